@@ -478,6 +478,124 @@ QMOE_API int32_t qmoe_launches_for(const qmoe_handle* h, int64_t T);
  * handle or T < 0. No counterpart on the pages: it only reports the plan. */
 QMOE_API int32_t qmoe_token_tile_for(const qmoe_handle* h, int64_t T);
 
+/* ---------------------------------------------------------------------------
+ * Dense operators beside the routed experts: 4-bit microscaling (MX4) rows and
+ * their product, and the gated feed-forward block of a shared expert with its
+ * backward pass (its forward computes qmoe_forward's shared_output; since
+ * y = routed(x) + shared(x), its gradients need nothing of the routed part).
+ * The pages name the formats and the sibling layers ("QLinearWoQ", "MoE")
+ * without such calls; the formulas below are the contract.
+ *
+ * These calls take no handle. All pointers are DEVICE pointers of the current
+ * device, borrowed until the enqueued work has run; outputs must not overlap
+ * inputs or each other. Work is enqueued on `stream` without waiting and can
+ * be captured into a graph. A bad argument returns QMOE_INVALID_ARGUMENT, a
+ * shape or type that is not built QMOE_UNSUPPORTED, before anything is
+ * enqueued; qmoe_dense_last_error has the text. A workspace is 256-byte
+ * aligned, of at least the size its _workspace_size function gives (0 for bad
+ * arguments), contents ignored on entry, and serves one call at a time: calls
+ * whose GPU work can overlap, replays of captured graphs among them, need one
+ * each.
+ */
+
+/* Text of the calling thread's last failed dense call ("" if none). */
+QMOE_API const char* qmoe_dense_last_error(void);
+
+/* Wait for `stream`, then read the device status word of a dense call's
+ * workspace: QMOE_OK, or QMOE_TIMEOUT when a bounded device wait of the last
+ * call that used it gave up (its results are then undefined). */
+QMOE_API qmoe_status qmoe_dense_read_device_status(const void* workspace, void* stream);
+
+/*
+ * qmoe_mx4_quantize -- rows x [rows, K] of dtype F32 or BF16, ldx >= K
+ * elements from row to row, to MX4:
+ *   codes  [rows, K/2]  uint8, two e2m1 codes per byte, even k in the low half
+ *   scales [rows, K/32] uint8, E8M0
+ * the layout of QMOE_WEIGHTS_MXFP4 (what qmoe_set_weights takes). A block is 32
+ * consecutive k; with m its largest magnitude, E = floor(log2 m) - 2, at least
+ * -127, the scale is the byte E + 127 and each code the e2m1 value nearest to
+ * x / 2^E: ties to the even code, magnitudes above 6 to 6, signs kept on
+ * zeros. m = 0 takes byte 0. A block that holds a NaN or an infinity takes
+ * byte 255 (NaN) and codes 0. K is a multiple of 32; x 16-byte aligned and
+ * ldx a multiple of 16 bytes; codes 4-byte aligned. rows = 0 is a no-op.
+ */
+QMOE_API qmoe_status qmoe_mx4_quantize(const void* x, int32_t dtype, int64_t rows, int64_t K, int64_t ldx,
+                                       uint8_t* codes, uint8_t* scales, void* stream);
+
+/*
+ * qmoe_mx4_dequantize -- the values of MX4 rows, x = e2m1(code) *
+ * 2^(scale - 127), rounded to dtype (exact unless it overflows to infinity); a
+ * scale byte of 255 gives NaN. Arguments as above, x written.
+ */
+QMOE_API qmoe_status qmoe_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K,
+                                         void* x, int32_t dtype, int64_t ldx, void* stream);
+
+/*
+ * qmoe_mx4_linear -- y [T, N] = deq(x) deq(w)^T + bias, both operands MX4 rows
+ * of length K (x: T rows, w: N rows), products exact, sums in fp32, rounded
+ * once to dtype (F32 or BF16, of y and bias). bias [N] or NULL. K is a
+ * multiple of 32; codes 16-byte and scales 4-byte aligned, y and bias aligned
+ * to their elements; T, N < 2^31. A row with a NaN scale gives NaN in every
+ * output it enters. T = 0 is a no-op.
+ */
+QMOE_API size_t qmoe_mx4_linear_workspace_size(int64_t T, int64_t N, int64_t K);
+QMOE_API qmoe_status qmoe_mx4_linear(int64_t T, int64_t N, int64_t K, const uint8_t* x_codes,
+                                     const uint8_t* x_scales, const uint8_t* w_codes, const uint8_t* w_scales,
+                                     const void* bias, void* y, int32_t dtype, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
+/*
+ * Gated feed-forward block, weights dense:
+ *   gu = x w1^T + b1   [T, 2I]; swiglu_fusion 1: columns 2i = gate, 2i + 1 =
+ *                      up; 2: [0, I) = gate, [I, 2I) = up
+ *   h  = act(g) * u    [T, I]; SWIGLU as in qmoe_config (alpha 0 reads as 1,
+ *                      limit <= 0 or non-finite: no clamp)
+ *   y  = h w2^T + b2   [T, H]
+ * NaN in g or u gives NaN in h. Sums are fp32; h (and the backward pass's
+ * gradient of gu) are rounded to bf16 where they become a product's operand.
+ */
+typedef struct qmoe_gated_ffn_config {
+    int64_t hidden_size;      /* H, a multiple of 8 */
+    int64_t inter_size;       /* I, a multiple of 8 */
+    int32_t activation_type;  /* QMOE_ACT_* */
+    int32_t swiglu_fusion;    /* 1 or 2 (any activation: the layout of w1) */
+    float activation_alpha;
+    float activation_beta;
+    float swiglu_limit;
+    int32_t gelu_mode;        /* QMOE_GELU_* */
+    int32_t act_dtype;        /* QMOE_DTYPE_BF16 (F32 is not built) */
+    int32_t reserved;         /* must be 0 */
+} qmoe_gated_ffn_config;
+
+/* Bytes of workspace for T tokens, forward (backward 0) or backward (1). */
+QMOE_API size_t qmoe_gated_ffn_workspace_size(const qmoe_gated_ffn_config* cfg, int64_t T, int32_t backward);
+
+/*
+ * qmoe_gated_ffn_forward -- x [T, H], w1 [2I, H], b1 [2I] or NULL, w2 [H, I],
+ * b2 [H] or NULL, y [T, H], all act_dtype; gu [T, 2I] fp32, in w1's row
+ * order, is written for the backward pass unless NULL (y does not depend on
+ * it). Tensors 16-byte, biases 2-byte aligned. T = 0 is a no-op.
+ */
+QMOE_API qmoe_status qmoe_gated_ffn_forward(const qmoe_gated_ffn_config* cfg, int64_t T, const void* x,
+                                            const void* w1, const void* b1, const void* w2, const void* b2,
+                                            float* gu, void* y, void* workspace, size_t workspace_bytes,
+                                            void* stream);
+
+/*
+ * qmoe_gated_ffn_backward -- from dy [T, H] and the forward's x, weights and
+ * gu: dh = dy w2; dgu = the activation's derivatives times dh (at a clamp's
+ * limit the slope is 1, beyond it 0; relu's slope at 0 is 0);
+ *   dx  [T, H]  = dgu w1        dw1 [2I, H] = dgu^T x    db1 [2I] = sum_t dgu
+ *                               dw2 [H, I]  = dy^T h     db2 [H]  = sum_t dy
+ * all act_dtype, written (not added to); any may be NULL to skip it. T = 0
+ * writes zeros to the weight and bias gradients. Results do not depend on
+ * which outputs are asked for, and are the same on every call.
+ */
+QMOE_API qmoe_status qmoe_gated_ffn_backward(const qmoe_gated_ffn_config* cfg, int64_t T, const void* dy,
+                                             const void* x, const void* w1, const void* w2, const float* gu,
+                                             void* dx, void* dw1, void* db1, void* dw2, void* db2,
+                                             void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

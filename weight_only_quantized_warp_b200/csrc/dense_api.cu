@@ -1,0 +1,313 @@
+// dense_api.cu -- C entry points of the dense operators declared in
+// include/qmoe.h: argument checks, workspace layout and launch sequences.
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+
+#include "dense.cuh"
+
+using namespace qmoe;
+
+namespace {
+
+thread_local char g_error[256] = "";
+
+qmoe_status bad(qmoe_status s, const char* fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_error, sizeof g_error, fmt, ap);
+    va_end(ap);
+    return s;
+}
+
+qmoe_status cuda_bad(cudaError_t e, const char* where) {
+    return bad(QMOE_CUDA_ERROR, "%s: %s", where, cudaGetErrorString(e));
+}
+
+bool misaligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) & (n - 1); }
+
+constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
+
+// The launches go to the current device: a tensor of another one is refused.
+qmoe_status on_current_device(const void* p) {
+    int dev = 0;
+    cudaPointerAttributes at;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaPointerGetAttributes(&at, p);
+    if (e != cudaSuccess) return cuda_bad(e, "device of the output");
+    if (at.type != cudaMemoryTypeDevice && at.type != cudaMemoryTypeManaged)
+        return bad(QMOE_INVALID_ARGUMENT, "not a device pointer");
+    if (at.type == cudaMemoryTypeDevice && at.device != dev)
+        return bad(QMOE_INVALID_ARGUMENT, "the output is on device %d, the current device is %d", at.device, dev);
+    return QMOE_OK;
+}
+
+qmoe_status check_workspace(const void* ws, size_t have, size_t need) {
+    if (!ws || misaligned(ws, 256)) return bad(QMOE_INVALID_ARGUMENT, "the workspace must be 256-byte aligned");
+    if (have < need) return bad(QMOE_INVALID_ARGUMENT, "workspace too small: %zu < %zu", have, need);
+    return QMOE_OK;
+}
+
+// Workspaces begin with the device status word; parts are 256-byte aligned.
+struct Layout {
+    size_t total = 256;
+    size_t take(size_t bytes) {
+        const size_t at = total;
+        total += (bytes + 255) & ~size_t(255);
+        return at;
+    }
+};
+
+qmoe_status check_mx4_rows(const void* x, int32_t dtype, int64_t rows, int64_t K, int64_t ldx, const void* codes,
+                           const void* scales) {
+    if (dtype != QMOE_DTYPE_F32 && dtype != QMOE_DTYPE_BF16)
+        return bad(QMOE_INVALID_ARGUMENT, "dtype must be F32 or BF16");
+    if (rows < 0 || K < 32 || K % 32) return bad(QMOE_INVALID_ARGUMENT, "rows >= 0 and K a positive multiple of 32");
+    if (K > kMaxDim || rows > kMaxDim || rows > (int64_t(1) << 48) / K)
+        return bad(QMOE_UNSUPPORTED, "rows or K too large");
+    const int per16 = dtype == QMOE_DTYPE_F32 ? 4 : 8;
+    if (rows > 1 && (ldx < K || ldx % per16 || ldx > (int64_t(1) << 40) / rows))
+        return bad(QMOE_INVALID_ARGUMENT, "ldx must be at least K and a multiple of 16 bytes");
+    if (rows == 0) return QMOE_OK;
+    if (!x || !codes || !scales) return bad(QMOE_INVALID_ARGUMENT, "x, codes and scales are required");
+    if (misaligned(x, 16) || misaligned(codes, 4))
+        return bad(QMOE_INVALID_ARGUMENT, "x must be 16-byte, codes 4-byte aligned");
+    return QMOE_OK;
+}
+
+// Checked configuration: the gate's parameters.
+qmoe_status check_ffn(const qmoe_gated_ffn_config* c, int64_t T, GateParams* g) {
+    if (!c) return bad(QMOE_INVALID_ARGUMENT, "cfg is required");
+    if (c->hidden_size < 1 || c->inter_size < 1 || T < 0)
+        return bad(QMOE_INVALID_ARGUMENT, "hidden_size and inter_size must be positive, T >= 0");
+    if (c->activation_type < QMOE_ACT_RELU || c->activation_type > QMOE_ACT_IDENTITY)
+        return bad(QMOE_INVALID_ARGUMENT, "unknown activation_type");
+    if (c->swiglu_fusion != 1 && c->swiglu_fusion != 2)
+        return bad(QMOE_INVALID_ARGUMENT, "swiglu_fusion must be 1 or 2");
+    if (c->gelu_mode != QMOE_GELU_ERF && c->gelu_mode != QMOE_GELU_TANH)
+        return bad(QMOE_INVALID_ARGUMENT, "unknown gelu_mode");
+    if (c->act_dtype != QMOE_DTYPE_F32 && c->act_dtype != QMOE_DTYPE_BF16)
+        return bad(QMOE_INVALID_ARGUMENT, "act_dtype must be BF16");
+    if (c->reserved) return bad(QMOE_INVALID_ARGUMENT, "reserved must be 0");
+    if (!std::isfinite(c->activation_alpha) || !std::isfinite(c->activation_beta))
+        return bad(QMOE_INVALID_ARGUMENT, "activation_alpha and activation_beta must be finite");
+    if (c->act_dtype == QMOE_DTYPE_F32) return bad(QMOE_UNSUPPORTED, "fp32 activations are not built");
+    if (c->hidden_size % 8 || c->inter_size % 8)
+        return bad(QMOE_UNSUPPORTED, "hidden_size and inter_size must be multiples of 8");
+    if (T > kMaxDim || c->hidden_size > kMaxDim / 2 || c->inter_size > kMaxDim / 2)
+        return bad(QMOE_UNSUPPORTED, "T, hidden_size or inter_size too large");
+    if (g) {
+        g->act = c->activation_type == QMOE_ACT_GELU && c->gelu_mode == QMOE_GELU_TANH ? kActGeluTanh
+                                                                                      : c->activation_type;
+        g->alpha = c->activation_alpha == 0.0f ? 1.0f : c->activation_alpha;
+        g->beta = c->activation_beta;
+        g->limit = c->swiglu_limit > 0.0f && std::isfinite(c->swiglu_limit) ? c->swiglu_limit : INFINITY;
+    }
+    return QMOE_OK;
+}
+
+struct FfnLayout : Layout {
+    size_t h = 0, dgu = 0, part = 0;
+    FfnLayout(const qmoe_gated_ffn_config& c, int64_t T, bool backward) {
+        h = take(size_t(T) * c.inter_size * 2);
+        if (backward) {
+            dgu = take(size_t(T) * c.inter_size * 4);
+            const size_t p1 = colsum_bytes(T, 2 * c.inter_size), p2 = colsum_bytes(T, c.hidden_size);
+            part = take(p1 > p2 ? p1 : p2);
+        }
+    }
+};
+
+DenseOperand rows_of(const void* p, int64_t ld) { return {p, nullptr, ld, 1}; }   // k along the row
+DenseOperand cols_of(const void* p, int64_t ld) { return {p, nullptr, 1, ld}; }   // k across the rows
+
+}  // namespace
+
+extern "C" {
+
+const char* qmoe_dense_last_error(void) { return g_error; }
+
+qmoe_status qmoe_dense_read_device_status(const void* workspace, void* stream) {
+    if (!workspace) return bad(QMOE_INVALID_ARGUMENT, "workspace is required");
+    int32_t v = 0;
+    cudaError_t e = cudaMemcpyAsync(&v, workspace, 4, cudaMemcpyDeviceToHost, (cudaStream_t)stream);
+    if (e == cudaSuccess) e = cudaStreamSynchronize((cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_bad(e, "read_device_status");
+    return v == 0 ? QMOE_OK : QMOE_TIMEOUT;
+}
+
+qmoe_status qmoe_mx4_quantize(const void* x, int32_t dtype, int64_t rows, int64_t K, int64_t ldx, uint8_t* codes,
+                              uint8_t* scales, void* stream) {
+    if (qmoe_status s = check_mx4_rows(x, dtype, rows, K, ldx, codes, scales)) return s;
+    if (rows == 0) return QMOE_OK;
+    if (qmoe_status s = on_current_device(codes)) return s;
+    const cudaError_t e = launch_mx4_quantize(x, dtype == QMOE_DTYPE_BF16, rows, K, rows > 1 ? ldx : K, codes, scales,
+                                              (cudaStream_t)stream);
+    return e == cudaSuccess ? QMOE_OK : cuda_bad(e, "mx4_quantize");
+}
+
+qmoe_status qmoe_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K, void* x,
+                                int32_t dtype, int64_t ldx, void* stream) {
+    if (qmoe_status s = check_mx4_rows(x, dtype, rows, K, ldx, codes, scales)) return s;
+    if (rows == 0) return QMOE_OK;
+    if (qmoe_status s = on_current_device(x)) return s;
+    const cudaError_t e = launch_mx4_dequantize(codes, scales, rows, K, x, dtype == QMOE_DTYPE_BF16,
+                                                rows > 1 ? ldx : K, (cudaStream_t)stream);
+    return e == cudaSuccess ? QMOE_OK : cuda_bad(e, "mx4_dequantize");
+}
+
+size_t qmoe_mx4_linear_workspace_size(int64_t T, int64_t N, int64_t K) {
+    if (T < 0 || N < 1 || K < 32 || K % 32 || T > kMaxDim || N > kMaxDim || K > kMaxDim) return 0;
+    return Layout().total;
+}
+
+qmoe_status qmoe_mx4_linear(int64_t T, int64_t N, int64_t K, const uint8_t* x_codes, const uint8_t* x_scales,
+                            const uint8_t* w_codes, const uint8_t* w_scales, const void* bias, void* y, int32_t dtype,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+    if (T < 0 || N < 1 || K < 32 || K % 32)
+        return bad(QMOE_INVALID_ARGUMENT, "T >= 0, N >= 1 and K a positive multiple of 32");
+    if (dtype != QMOE_DTYPE_F32 && dtype != QMOE_DTYPE_BF16)
+        return bad(QMOE_INVALID_ARGUMENT, "dtype must be F32 or BF16");
+    if (T > kMaxDim || N > kMaxDim || K > kMaxDim) return bad(QMOE_UNSUPPORTED, "T, N or K too large");
+    if (T == 0) return QMOE_OK;
+    if (!x_codes || !x_scales || !w_codes || !w_scales || !y)
+        return bad(QMOE_INVALID_ARGUMENT, "codes, scales and y are required");
+    const int es = dtype == QMOE_DTYPE_F32 ? 4 : 2;
+    if (misaligned(x_codes, 16) || misaligned(w_codes, 16) || misaligned(x_scales, 4) || misaligned(w_scales, 4))
+        return bad(QMOE_INVALID_ARGUMENT, "codes must be 16-byte, scales 4-byte aligned");
+    if (misaligned(y, es) || misaligned(bias, es))
+        return bad(QMOE_INVALID_ARGUMENT, "y and bias must be aligned to their elements");
+    if (qmoe_status s = check_workspace(workspace, workspace_bytes, qmoe_mx4_linear_workspace_size(T, N, K))) return s;
+    if (qmoe_status s = on_current_device(y)) return s;
+    DenseArgs a{};
+    a.a = {x_codes, x_scales, 0, 0};
+    a.b = {w_codes, w_scales, 0, 0};
+    a.M = T;
+    a.N = N;
+    a.K = K;
+    a.mx4 = 1;
+    a.epi = kEpiStore;
+    a.out_f32 = dtype == QMOE_DTYPE_F32;
+    a.bias = bias;
+    a.out = y;
+    cudaError_t e = cudaMemsetAsync(workspace, 0, 4, (cudaStream_t)stream);
+    if (e == cudaSuccess) e = launch_dense(a, (cudaStream_t)stream);
+    return e == cudaSuccess ? QMOE_OK : cuda_bad(e, "mx4_linear");
+}
+
+size_t qmoe_gated_ffn_workspace_size(const qmoe_gated_ffn_config* cfg, int64_t T, int32_t backward) {
+    if (check_ffn(cfg, T, nullptr)) return 0;
+    return FfnLayout(*cfg, T, backward != 0).total;
+}
+
+qmoe_status qmoe_gated_ffn_forward(const qmoe_gated_ffn_config* cfg, int64_t T, const void* x, const void* w1,
+                                   const void* b1, const void* w2, const void* b2, float* gu, void* y,
+                                   void* workspace, size_t workspace_bytes, void* stream) {
+    GateParams gate;
+    if (qmoe_status s = check_ffn(cfg, T, &gate)) return s;
+    if (T == 0) return QMOE_OK;
+    if (!x || !w1 || !w2 || !y) return bad(QMOE_INVALID_ARGUMENT, "x, w1, w2 and y are required");
+    if (misaligned(x, 16) || misaligned(w1, 16) || misaligned(w2, 16) || misaligned(y, 16) || misaligned(gu, 16) ||
+        misaligned(b1, 2) || misaligned(b2, 2))
+        return bad(QMOE_INVALID_ARGUMENT, "tensors must be 16-byte, biases 2-byte aligned");
+    const FfnLayout l(*cfg, T, false);
+    if (qmoe_status s = check_workspace(workspace, workspace_bytes, l.total)) return s;
+    if (qmoe_status s = on_current_device(y)) return s;
+    cudaStream_t st = (cudaStream_t)stream;
+    const int64_t H = cfg->hidden_size, I = cfg->inter_size;
+    void* h = (char*)workspace + l.h;
+    DenseArgs a{};
+    a.a = rows_of(x, H);
+    a.b = rows_of(w1, H);
+    a.M = T;
+    a.N = 2 * I;
+    a.K = H;
+    a.epi = kEpiGate;
+    a.bias = b1;
+    a.out = h;
+    a.gu = gu;
+    a.gate = gate;
+    a.interleaved = cfg->swiglu_fusion == 1;
+    cudaError_t e = cudaMemsetAsync(workspace, 0, 4, st);
+    if (e == cudaSuccess) e = launch_dense(a, st);
+    DenseArgs d{};
+    d.a = rows_of(h, I);
+    d.b = rows_of(w2, I);
+    d.M = T;
+    d.N = H;
+    d.K = I;
+    d.epi = kEpiStore;
+    d.bias = b2;
+    d.out = y;
+    if (e == cudaSuccess) e = launch_dense(d, st);
+    return e == cudaSuccess ? QMOE_OK : cuda_bad(e, "gated_ffn_forward");
+}
+
+qmoe_status qmoe_gated_ffn_backward(const qmoe_gated_ffn_config* cfg, int64_t T, const void* dy, const void* x,
+                                    const void* w1, const void* w2, const float* gu, void* dx, void* dw1, void* db1,
+                                    void* dw2, void* db2, void* workspace, size_t workspace_bytes, void* stream) {
+    GateParams gate;
+    if (qmoe_status s = check_ffn(cfg, T, &gate)) return s;
+    const int64_t H = cfg->hidden_size, I = cfg->inter_size;
+    cudaStream_t st = (cudaStream_t)stream;
+    if (misaligned(dx, 16) || misaligned(dw1, 16) || misaligned(dw2, 16) || misaligned(db1, 2) || misaligned(db2, 2))
+        return bad(QMOE_INVALID_ARGUMENT, "gradients must be 16-byte, bias gradients 2-byte aligned");
+    void* outs[] = {T ? dx : nullptr, dw1, db1, dw2, db2};
+    const size_t bytes[] = {0, size_t(4 * I) * H, size_t(4 * I), size_t(2 * I) * H, size_t(2 * H)};
+    void* first = nullptr;
+    for (void* o : outs)
+        if (o && !first) first = o;
+    if (!first) return QMOE_OK;
+    if (T == 0) {  // empty sums
+        if (qmoe_status s = on_current_device(first)) return s;
+        for (int i = 1; i < 5; ++i)
+            if (outs[i])
+                if (cudaError_t e = cudaMemsetAsync(outs[i], 0, bytes[i], st)) return cuda_bad(e, "gated_ffn_backward");
+        return QMOE_OK;
+    }
+    if (!dy || !x || !w1 || !w2 || !gu) return bad(QMOE_INVALID_ARGUMENT, "dy, x, w1, w2 and gu are required");
+    if (misaligned(dy, 16) || misaligned(x, 16) || misaligned(w1, 16) || misaligned(w2, 16) || misaligned(gu, 16))
+        return bad(QMOE_INVALID_ARGUMENT, "tensors must be 16-byte aligned");
+    const FfnLayout l(*cfg, T, true);
+    if (qmoe_status s = check_workspace(workspace, workspace_bytes, l.total)) return s;
+    if (qmoe_status s = on_current_device(first)) return s;
+    char* ws = (char*)workspace;
+    void *h = ws + l.h, *dgu = ws + l.dgu;
+    float* part = (float*)(ws + l.part);
+    cudaError_t e = cudaMemsetAsync(workspace, 0, 4, st);
+    auto product = [&](DenseOperand oa, DenseOperand ob, int64_t M, int64_t N, int64_t K, void* out) {
+        if (e != cudaSuccess || !out) return;
+        DenseArgs a{};
+        a.a = oa;
+        a.b = ob;
+        a.M = M;
+        a.N = N;
+        a.K = K;
+        a.epi = kEpiStore;
+        a.out = out;
+        e = launch_dense(a, st);
+    };
+    if (e == cudaSuccess && (dx || dw1 || db1 || dw2)) {
+        DenseArgs a{};
+        a.a = rows_of(dy, H);
+        a.b = cols_of(w2, I);
+        a.M = T;
+        a.N = I;
+        a.K = H;
+        a.epi = kEpiGateBwd;
+        a.out = h;
+        a.gu = const_cast<float*>(gu);
+        a.dgu = dgu;
+        a.gate = gate;
+        a.interleaved = cfg->swiglu_fusion == 1;
+        e = launch_dense(a, st);
+    }
+    product(cols_of(dy, H), cols_of(h, I), H, I, T, dw2);
+    product(rows_of(dgu, 2 * I), cols_of(w1, H), T, H, 2 * I, dx);
+    product(cols_of(dgu, 2 * I), cols_of(x, H), 2 * I, H, T, dw1);
+    if (e == cudaSuccess && db1) e = launch_colsum(dgu, T, 2 * I, db1, part, st);
+    if (e == cudaSuccess && db2) e = launch_colsum(dy, T, H, db2, part, st);
+    return e == cudaSuccess ? QMOE_OK : cuda_bad(e, "gated_ffn_backward");
+}
+
+}  // extern "C"

@@ -42,7 +42,10 @@ EXPORTS = ("qmoe_create", "qmoe_set_weights", "qmoe_workspace_size", "qmoe_forwa
            "qmoe_set_option", "qmoe_forward_noalloc", "qmoe_noalloc_scratch_bytes",
            "qmoe_noalloc_read_device_status", "qmoe_set_score_correction_bias",
            "qmoe_quantize_act_i8", "qmoe_ep_state_bytes", "qmoe_ep_dispatch",
-           "qmoe_ep_rows_workspace_size", "qmoe_ep_expert_rows", "qmoe_ep_combine")
+           "qmoe_ep_rows_workspace_size", "qmoe_ep_expert_rows", "qmoe_ep_combine",
+           "qmoe_dense_last_error", "qmoe_dense_read_device_status", "qmoe_mx4_quantize",
+           "qmoe_mx4_dequantize", "qmoe_mx4_linear_workspace_size", "qmoe_mx4_linear",
+           "qmoe_gated_ffn_workspace_size", "qmoe_gated_ffn_forward", "qmoe_gated_ffn_backward")
 QMOE_OPT_PATH, QMOE_OPT_WAIT_LIMIT_NS, QMOE_OPT_TEST_WITHHOLD, QMOE_OPT_PDL, QMOE_OPT_DECODE_TILES = 1, 2, 3, 4, 5
 
 
@@ -61,6 +64,14 @@ class qmoe_config(ctypes.Structure):
                 ("routed_scaling_factor", ctypes.c_float), ("apply_router_weight_on_input", ctypes.c_int32),
                 ("weight_format", ctypes.c_int32), ("compute_mode", ctypes.c_int32),
                 ("expert_output_scale", ctypes.c_float), ("gelu_mode", ctypes.c_int32)]
+
+
+class qmoe_gated_ffn_config(ctypes.Structure):
+    _fields_ = [("hidden_size", ctypes.c_int64), ("inter_size", ctypes.c_int64),
+                ("activation_type", ctypes.c_int32), ("swiglu_fusion", ctypes.c_int32),
+                ("activation_alpha", ctypes.c_float), ("activation_beta", ctypes.c_float),
+                ("swiglu_limit", ctypes.c_float), ("gelu_mode", ctypes.c_int32),
+                ("act_dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 _vp, _i64, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t
@@ -115,6 +126,26 @@ lib.qmoe_ep_expert_rows.restype = ctypes.c_int
 lib.qmoe_ep_expert_rows.argtypes = [_vp, _i64, _vp, _vp, ctypes.c_int32, _vp, _vp, _sz, _vp]
 lib.qmoe_ep_combine.restype = ctypes.c_int
 lib.qmoe_ep_combine.argtypes = [_vp, _i64, _vp, _vp, _vp, _vp, _vp]
+
+_i32, _ffn = ctypes.c_int32, ctypes.POINTER(qmoe_gated_ffn_config)
+lib.qmoe_dense_last_error.restype = ctypes.c_char_p
+lib.qmoe_dense_last_error.argtypes = []
+lib.qmoe_dense_read_device_status.restype = ctypes.c_int
+lib.qmoe_dense_read_device_status.argtypes = [_vp, _vp]
+lib.qmoe_mx4_quantize.restype = ctypes.c_int
+lib.qmoe_mx4_quantize.argtypes = [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _vp]
+lib.qmoe_mx4_dequantize.restype = ctypes.c_int
+lib.qmoe_mx4_dequantize.argtypes = [_vp, _vp, _i64, _i64, _vp, _i32, _i64, _vp]
+lib.qmoe_mx4_linear_workspace_size.restype = _sz
+lib.qmoe_mx4_linear_workspace_size.argtypes = [_i64, _i64, _i64]
+lib.qmoe_mx4_linear.restype = ctypes.c_int
+lib.qmoe_mx4_linear.argtypes = [_i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _sz, _vp]
+lib.qmoe_gated_ffn_workspace_size.restype = _sz
+lib.qmoe_gated_ffn_workspace_size.argtypes = [_ffn, _i64, _i32]
+lib.qmoe_gated_ffn_forward.restype = ctypes.c_int
+lib.qmoe_gated_ffn_forward.argtypes = [_ffn, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
+lib.qmoe_gated_ffn_backward.restype = ctypes.c_int
+lib.qmoe_gated_ffn_backward.argtypes = [_ffn, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
 
 
 class QMoEError(RuntimeError):
@@ -293,6 +324,51 @@ def qmoe_ep_combine(h, T, expert_out, state, shared_output, y, stream=None):
     outputs that came back in dispatch order."""
     _check(lib.qmoe_ep_combine(h, T, _ptr(expert_out), _ptr(state), _ptr(shared_output), _ptr(y),
                                _stream(stream)), h)
+
+
+def _check_dense(status: int):
+    if status != QMOE_OK:
+        raise QMoEError(status, lib.qmoe_dense_last_error().decode())
+
+
+def qmoe_dense_read_device_status(workspace, stream=None) -> int:
+    return int(lib.qmoe_dense_read_device_status(_ptr(workspace), _stream(stream)))
+
+
+def qmoe_mx4_quantize(x, dtype: int, rows: int, K: int, ldx: int, codes, scales, stream=None):
+    """Rows x (a device address, or a contiguous tensor) to MX4 codes
+    [rows, K/2] and E8M0 scales [rows, K/32]; see include/qmoe.h."""
+    _check_dense(lib.qmoe_mx4_quantize(_ptr(x), dtype, rows, K, ldx, _ptr(codes), _ptr(scales), _stream(stream)))
+
+
+def qmoe_mx4_dequantize(codes, scales, rows: int, K: int, x, dtype: int, ldx: int, stream=None):
+    _check_dense(lib.qmoe_mx4_dequantize(_ptr(codes), _ptr(scales), rows, K, _ptr(x), dtype, ldx, _stream(stream)))
+
+
+def qmoe_mx4_linear_workspace_size(T: int, N: int, K: int) -> int:
+    return int(lib.qmoe_mx4_linear_workspace_size(T, N, K))
+
+
+def qmoe_mx4_linear(T, N, K, x_codes, x_scales, w_codes, w_scales, bias, y, dtype, workspace, workspace_bytes,
+                    stream=None):
+    _check_dense(lib.qmoe_mx4_linear(T, N, K, _ptr(x_codes), _ptr(x_scales), _ptr(w_codes), _ptr(w_scales),
+                                     _ptr(bias), _ptr(y), dtype, _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def qmoe_gated_ffn_workspace_size(cfg: qmoe_gated_ffn_config, T: int, backward: bool) -> int:
+    return int(lib.qmoe_gated_ffn_workspace_size(ctypes.byref(cfg), T, int(backward)))
+
+
+def qmoe_gated_ffn_forward(cfg, T, x, w1, b1, w2, b2, gu, y, workspace, workspace_bytes, stream=None):
+    _check_dense(lib.qmoe_gated_ffn_forward(ctypes.byref(cfg), T, _ptr(x), _ptr(w1), _ptr(b1), _ptr(w2), _ptr(b2),
+                                            _ptr(gu), _ptr(y), _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def qmoe_gated_ffn_backward(cfg, T, dy, x, w1, w2, gu, dx, dw1, db1, dw2, db2, workspace, workspace_bytes,
+                            stream=None):
+    _check_dense(lib.qmoe_gated_ffn_backward(ctypes.byref(cfg), T, _ptr(dy), _ptr(x), _ptr(w1), _ptr(w2), _ptr(gu),
+                                             _ptr(dx), _ptr(dw1), _ptr(db1), _ptr(dw2), _ptr(db2), _ptr(workspace),
+                                             workspace_bytes, _stream(stream)))
 
 
 # ------------------------------------------------------------- torch plumbing
