@@ -109,8 +109,12 @@ struct DenseArgs {
     void* dgu;             // kEpiGateBwd
     GateParams gate;
     int interleaved;       // gate and up interleaved in w1 / gu (else concatenated)
+    int32_t* status;       // workspace status word; reset by the call's first product
+    int reset_status;
+    void* scratch;         // mx4: dense_pair_workspace bytes
 };
-cudaError_t launch_dense(const DenseArgs& a, cudaStream_t st);
+size_t dense_pair_workspace(int64_t M, int64_t N, int64_t K);  // re-laid MX4 scales
+cudaError_t launch_dense_pair(const DenseArgs& a, cudaStream_t st);
 
 // out[n] = sum_m x[m, n] (x [M, N] bf16) in a fixed order; part: workspace of
 // colsum_bytes(M, N).

@@ -158,7 +158,9 @@ qmoe_status qmoe_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int
 
 size_t qmoe_mx4_linear_workspace_size(int64_t T, int64_t N, int64_t K) {
     if (T < 0 || N < 1 || K < 32 || K % 32 || T > kMaxDim || N > kMaxDim || K > kMaxDim) return 0;
-    return Layout().total;
+    Layout l;
+    l.take(dense_pair_workspace(T, N, K));
+    return l.total;
 }
 
 qmoe_status qmoe_mx4_linear(int64_t T, int64_t N, int64_t K, const uint8_t* x_codes, const uint8_t* x_scales,
@@ -190,8 +192,10 @@ qmoe_status qmoe_mx4_linear(int64_t T, int64_t N, int64_t K, const uint8_t* x_co
     a.out_f32 = dtype == QMOE_DTYPE_F32;
     a.bias = bias;
     a.out = y;
-    cudaError_t e = cudaMemsetAsync(workspace, 0, 4, (cudaStream_t)stream);
-    if (e == cudaSuccess) e = launch_dense(a, (cudaStream_t)stream);
+    a.status = (int32_t*)workspace;
+    a.reset_status = 1;
+    a.scratch = (char*)workspace + Layout().total;
+    const cudaError_t e = launch_dense_pair(a, (cudaStream_t)stream);
     return e == cudaSuccess ? QMOE_OK : cuda_bad(e, "mx4_linear");
 }
 
@@ -228,8 +232,9 @@ qmoe_status qmoe_gated_ffn_forward(const qmoe_gated_ffn_config* cfg, int64_t T, 
     a.gu = gu;
     a.gate = gate;
     a.interleaved = cfg->swiglu_fusion == 1;
-    cudaError_t e = cudaMemsetAsync(workspace, 0, 4, st);
-    if (e == cudaSuccess) e = launch_dense(a, st);
+    a.status = (int32_t*)workspace;
+    a.reset_status = 1;
+    cudaError_t e = launch_dense_pair(a, st);
     DenseArgs d{};
     d.a = rows_of(h, I);
     d.b = rows_of(w2, I);
@@ -239,7 +244,8 @@ qmoe_status qmoe_gated_ffn_forward(const qmoe_gated_ffn_config* cfg, int64_t T, 
     d.epi = kEpiStore;
     d.bias = b2;
     d.out = y;
-    if (e == cudaSuccess) e = launch_dense(d, st);
+    d.status = (int32_t*)workspace;
+    if (e == cudaSuccess) e = launch_dense_pair(d, st);
     return e == cudaSuccess ? QMOE_OK : cuda_bad(e, "gated_ffn_forward");
 }
 
@@ -285,7 +291,8 @@ qmoe_status qmoe_gated_ffn_backward(const qmoe_gated_ffn_config* cfg, int64_t T,
         a.K = K;
         a.epi = kEpiStore;
         a.out = out;
-        e = launch_dense(a, st);
+        a.status = (int32_t*)workspace;
+        e = launch_dense_pair(a, st);
     };
     if (e == cudaSuccess && (dx || dw1 || db1 || dw2)) {
         DenseArgs a{};
@@ -300,7 +307,8 @@ qmoe_status qmoe_gated_ffn_backward(const qmoe_gated_ffn_config* cfg, int64_t T,
         a.dgu = dgu;
         a.gate = gate;
         a.interleaved = cfg->swiglu_fusion == 1;
-        e = launch_dense(a, st);
+        a.status = (int32_t*)workspace;
+        e = launch_dense_pair(a, st);
     }
     product(cols_of(dy, H), cols_of(h, I), H, I, T, dw2);
     product(rows_of(dgu, 2 * I), cols_of(w1, H), T, H, 2 * I, dx);

@@ -1,0 +1,552 @@
+// dense_pair.cu -- the dense operators' products on tcgen05 CTA pairs (sm_100a).
+//
+// D[m, n] = sum_k A(m, k) B(n, k). Two CTAs of a cluster work on one 256 x BN
+// tile (cta_group::2): each loads its 128 rows of A and its half of B's rows,
+// so a tile's operand bytes per MAC are half of what a single CTA with the
+// same accumulators would load, and accumulates its 128 rows x BN columns in
+// tensor memory. Two accumulators alternate, so the epilogue of one tile runs
+// under the MMAs of the next. Tiles are walked in groups of kGroupM tile rows
+// by all columns, so that the operands of the tiles in flight stay in L2.
+//
+// Operands come by TMA in stages of 128 bytes of k per row (64 bf16 or 256
+// e2m1) into 128-byte swizzled lines; ends of M, N and K are zero-filled by
+// the copies. Where the reduction runs across the rows of a matrix in memory
+// (the backward pass: w2 and w1 as B of dh and dx, all operands of the weight
+// gradients) the stage is 64 k lines of 64 rows and the descriptor says
+// MN-major; nothing is transposed in memory.
+//
+// kind::mxf4 (MX4): products of e2m1 values with both E8M0 scales applied by
+// the tensor core, two scales per row and MMA (64 k). Scales are copied with
+// each stage from a re-laid array (see mx4_tile_scales_kernel) and from shared
+// to tensor memory by tcgen05.cp ahead of the stage's MMAs. BN is 240, not
+// 256: two 240-column accumulators leave 32 columns for a stage's scales.
+//
+// Gate epilogue: B's first half of a tile is 128 gate rows and the second 128
+// up rows (one per CTA), so a thread holds gate and up of the same column.
+//
+// Warps (384 threads): 0 TMA, 1 MMA issue (leader CTA) and tensor memory,
+// 4-11 epilogue. Every wait is bounded (then QMOE_TIMEOUT in the status word,
+// every role leaves its loop).
+#include "dense_tc.cuh"
+
+namespace qmoe {
+namespace {
+
+constexpr int kPThreads = 384;
+constexpr int kPEpi0 = 4, kPEpiWarps = 8;
+constexpr int kGroupM = 8;
+constexpr int kABytes = 128 * 128;  // one CTA's A rows of a stage
+
+struct PairArgs {
+    int64_t M, N, K;       // N: result columns (h columns for the gate)
+    int tiles_m, tiles_n, nks, z_b, chunks;
+    int epi, out_f32, interleaved, vec_out;
+    const void* bias;
+    void* out;
+    float* gu;
+    void* dgu;
+    GateParams gate;
+    int32_t* status;
+    int reset_status;
+};
+
+template <bool MX4>
+struct PairCfg {
+    static constexpr int BN = MX4 ? 240 : 256;
+    static constexpr int kB = BN / 2 * 128;
+    static constexpr int kSA = MX4 ? 1024 : 0, kSB = MX4 ? 2048 : 0;
+    static constexpr int kStage = kABytes + kB + kSA + kSB;
+    static constexpr int kStages = 6;
+    static constexpr int kBarOff = kStages * kStage;
+    static constexpr int kSmem = kBarOff + 1024 + 1024;
+    static_assert(kStage % 1024 == 0 && kSmem <= 227 * 1024, "stages");
+};
+
+__device__ __forceinline__ void pair_tile(const PairArgs& a, int t, int& tm, int& tn) {
+    const int per = kGroupM * a.tiles_n;
+    const int g = t / per, m0 = g * kGroupM, gm = min(a.tiles_m - m0, kGroupM), r = t - g * per;
+    tm = m0 + r % gm;
+    tn = r / gm;
+}
+
+// 32 results of one row, columns c0 .. c0 + 31 of an [*, N] bf16 array.
+__device__ __forceinline__ void store32_bf16(__nv_bfloat16* row, int64_t c0, int64_t N, bool vec, const float (&v)[32]) {
+    if (vec && c0 + 32 <= N) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint4*>(row + c0 + 8 * i) =
+                make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
+                           pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (c0 + i < N) row[c0 + i] = __float2bfloat16_rn(v[i]);
+    }
+}
+
+__device__ __forceinline__ void store32_f32(float* row, int64_t c0, int64_t N, bool vec, const float (&v)[32]) {
+    if (vec && c0 + 32 <= N) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<float4*>(row + c0 + 4 * i) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (c0 + i < N) row[c0 + i] = v[i];
+    }
+}
+
+template <bool MX4, bool AMN, bool BMN, int EPI>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
+    dense_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
+                      const __grid_constant__ CUtensorMap samap, const __grid_constant__ CUtensorMap sbmap,
+                      const PairArgs a) {
+    using C = PairCfg<MX4>;
+    constexpr int ST = C::kStages, BN = C::BN;
+    extern __shared__ uint8_t smem_raw[];
+    // the dynamic segment starts at the same address in both CTAs, so the
+    // aligned offsets agree
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cluster_rank();
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
+    uint64_t* empty = full + ST;
+    uint64_t* accf = empty + ST;
+    uint64_t* acce = accf + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acce + 2);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    if (tid == 0) {
+        for (int s = 0; s < ST; ++s) {
+            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&empty[s]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_u32(&accf[b]), 1);
+            mbar_init(smem_u32(&acce[b]), 2 * kPEpiWarps);
+        }
+        *abort_flag = 0;
+        if (a.reset_status && blockIdx.x == 0) *a.status = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "r"(512));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    }
+    tc_fence_before();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int total = a.tiles_m * a.tiles_n, step = gridDim.x / 2;
+
+    if (warp == 0) {
+        // ------------------------------------------------------- producer
+        const uint32_t e = elect_one();
+        int st = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (int t = blockIdx.x / 2; ok && t < total; t += step) {
+            int tm, tn;
+            pair_tile(a, t, tm, tn);
+            const int m0 = tm * 256 + int(rank) * 128;
+            const int n0 = EPI == kEpiGate ? tn * 128 : tn * BN + int(rank) * (BN / 2);
+            const int zb = EPI == kEpiGate ? int(rank) : 0;
+            for (int ks = 0; ks < a.nks; ++ks) {
+                if (!warp_wait(smem_u32(&empty[st]), ph ^ 1u, abort_flag, a.status, kTimeoutNs)) { ok = false; break; }
+                const uint32_t sa = smem_u32(smem + st * C::kStage), sb = sa + kABytes;
+                const uint32_t fb = map_rank(smem_u32(&full[st]), 0);
+                if (rank == 0) mbar_expect_tx_e(smem_u32(&full[st]), 2 * C::kStage, e);
+                if (AMN) {
+                    tma_3d_pair_e(sa, &amap, m0, ks * 64, 0, fb, e);
+                    tma_3d_pair_e(sa + 8192, &amap, m0 + 64, ks * 64, 0, fb, e);
+                } else {
+                    tma_3d_pair_e(sa, &amap, ks * (MX4 ? 128 : 64), m0, 0, fb, e);
+                }
+                if (BMN) {
+                    tma_3d_pair_e(sb, &bmap, n0, ks * 64, 0, fb, e);
+                    tma_3d_pair_e(sb + 8192, &bmap, n0 + 64, ks * 64, 0, fb, e);
+                } else {
+                    tma_3d_pair_e(sb, &bmap, ks * (MX4 ? 128 : 64), n0, zb, fb, e);
+                }
+                if (MX4) {
+                    tma_3d_pair_e(sb + C::kB, &samap, 0, (m0 >> 7) * (a.chunks >> 1) + ks, 0, fb, e);
+                    tma_3d_pair_e(sb + C::kB + C::kSA, &sbmap, 0, tn * a.chunks + 2 * ks, 0, fb, e);
+                }
+                if (++st == ST) { st = 0; ph ^= 1u; }
+            }
+        }
+    } else if (warp == 1 && rank == 0) {
+        // ------------------------------------------------------- MMA issue
+        const uint32_t e = elect_one();
+        int st = 0, acc = 0;
+        uint32_t ph = 0, cph = 0;
+        bool ok = true;
+        const uint32_t tscale = tmem + 2 * BN;  // MX4: A chunk 0, 1 (4 columns each), B chunk 0, 1 (8 each)
+        for (int t = blockIdx.x / 2; ok && t < total; t += step) {
+            if (!warp_wait_cluster(smem_u32(&acce[acc]), cph ^ 1u, abort_flag, a.status)) break;
+            tc_fence_after();
+            const uint32_t d = tmem + uint32_t(acc * BN);
+            for (int ks = 0; ks < a.nks; ++ks) {
+                if (!warp_wait_cluster(smem_u32(&full[st]), ph, abort_flag, a.status)) { ok = false; break; }
+                tc_fence_after();
+                const uint32_t sa = smem_u32(smem + st * C::kStage), sb = sa + kABytes;
+                const uint32_t acc0 = ks > 0 ? 1u : 0u;
+                if constexpr (MX4) {
+                    const uint32_t ssa = sb + C::kB, ssb = ssa + C::kSA;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        cp_scales_pair_e(tscale + 4 * j, desc_scales(ssa + 512 * j), e);
+                        cp_scales_pair_e(tscale + 8 + 8 * j, desc_scales(ssb + 1024 * j), e);
+                        cp_scales_pair_e(tscale + 12 + 8 * j, desc_scales(ssb + 1024 * j + 512), e);
+                    }
+                    const uint64_t ad = desc_sw128(sa), bd = desc_sw128(sb);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_mx4_pair_e(d, ad + uint64_t(2 * kk), bd + uint64_t(2 * kk), idesc_mx4(256, BN, 2 * (kk & 1)),
+                                       tscale + 4 * (kk >> 1), tscale + 8 + 8 * (kk >> 1), kk > 0 ? 1u : acc0, e);
+                } else {
+                    const uint64_t ad = AMN ? desc_mn128(sa) : desc_sw128(sa);
+                    const uint64_t bd = BMN ? desc_mn128(sb) : desc_sw128(sb);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)  // 16 k: 32 bytes into each line, or 16 lines on
+                        mma_bf16_pair_e(d, ad + uint64_t((AMN ? 128 : 2) * kk), bd + uint64_t((BMN ? 128 : 2) * kk),
+                                        idesc_f16(256, BN, AMN, BMN), kk > 0 ? 1u : acc0, e);
+                }
+                mma_commit_pair_e(smem_u32(&empty[st]), e);
+                if (++st == ST) { st = 0; ph ^= 1u; }
+            }
+            if (!ok) break;
+            mma_commit_pair_e(smem_u32(&accf[acc]), e);
+            if (++acc == 2) { acc = 0; cph ^= 1u; }
+        }
+    } else if (warp >= kPEpi0) {
+        // ------------------------------------------------------- epilogue
+        const int qd = warp & 3, half = (warp - kPEpi0) >> 2;
+        int acc = 0;
+        uint32_t cph = 0;
+        for (int t = blockIdx.x / 2; t < total; t += step) {
+            int tm, tn;
+            pair_tile(a, t, tm, tn);
+            if (!warp_wait(smem_u32(&accf[acc]), cph, abort_flag, a.status, kTimeoutNs)) break;
+            tc_fence_after();
+            const uint32_t tb = tmem + (uint32_t(qd * 32) << 16) + uint32_t(acc * BN);
+            const int64_t m = int64_t(tm) * 256 + rank * 128 + qd * 32 + lane;
+            const bool row = m < a.M;
+            if (EPI == kEpiStore) {
+                for (int c = half * 32; c < BN; c += 64) {
+                    const int64_t n = int64_t(tn) * BN + c;
+                    if (n >= a.N) break;  // uniform over the warp
+                    float v[32];
+                    if (BN - c >= 32) {
+                        uint32_t r[32];
+                        tmem_ld32(tb + uint32_t(c), r);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+                    } else {
+                        float w[16];
+                        tmem_ld16(tb + uint32_t(c), w);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = i < 16 ? w[i & 15] : 0.0f;
+                    }
+                    // the tile's last columns end inside a chunk when BN is not a multiple of 32
+                    const int64_t end = min(a.N, int64_t(tn + 1) * BN);
+                    if (a.bias) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (n + i < end)
+                                v[i] += a.out_f32 ? __ldg((const float*)a.bias + n + i)
+                                                  : __bfloat162float(((const __nv_bfloat16*)a.bias)[n + i]);
+                    }
+                    if (row) {
+                        if (a.out_f32) store32_f32((float*)a.out + m * a.N, n, end, a.vec_out, v);
+                        else store32_bf16((__nv_bfloat16*)a.out + m * a.N, n, end, a.vec_out, v);
+                    }
+                }
+            } else if (EPI == kEpiGate) {
+                for (int c = half * 32; c < 128; c += 64) {
+                    const int64_t n = int64_t(tn) * 128 + c;
+                    if (n >= a.N) break;
+                    uint32_t rg[32], ru[32];
+                    tmem_ld32(tb + uint32_t(c), rg);
+                    tmem_ld32(tb + uint32_t(128 + c), ru);
+                    tmem_wait_ld();
+                    float g[32], u[32], h[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        g[i] = __uint_as_float(rg[i]);
+                        u[i] = __uint_as_float(ru[i]);
+                    }
+                    if (a.bias) {
+                        const __nv_bfloat16* b = (const __nv_bfloat16*)a.bias;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (n + i < a.N) {
+                                g[i] += __bfloat162float(b[a.interleaved ? 2 * (n + i) : n + i]);
+                                u[i] += __bfloat162float(b[a.interleaved ? 2 * (n + i) + 1 : a.N + n + i]);
+                            }
+                    }
+                    if (row && a.gu) {
+                        float* gr = a.gu + m * 2 * a.N;
+                        if (a.interleaved) {  // N is a multiple of 8: whole groups of four pairs
+#pragma unroll
+                            for (int i = 0; i < 32; i += 2)
+                                if (n + i < a.N)
+                                    *reinterpret_cast<float4*>(gr + 2 * (n + i)) = make_float4(g[i], u[i], g[i + 1], u[i + 1]);
+                        } else {
+                            store32_f32(gr, n, a.N, true, g);
+                            store32_f32(gr + a.N, n, a.N, true, u);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) h[i] = gate_value(a.gate, g[i], u[i]);
+                    if (row) store32_bf16((__nv_bfloat16*)a.out + m * a.N, n, a.N, true, h);
+                }
+            } else {
+                for (int c = half * 32; c < BN; c += 64) {
+                    const int64_t n = int64_t(tn) * BN + c;
+                    if (n >= a.N) break;
+                    uint32_t rd[32];
+                    tmem_ld32(tb + uint32_t(c), rd);
+                    tmem_wait_ld();
+                    const float* gr = a.gu + m * 2 * a.N;
+                    __nv_bfloat16* dr = (__nv_bfloat16*)a.dgu + m * 2 * a.N;
+                    __nv_bfloat16* hr = (__nv_bfloat16*)a.out + m * a.N;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8) {  // N is a multiple of 8
+                        if (!row || n + i >= a.N) break;
+                        float g[8], u[8];
+                        if (a.interleaved) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const float4 w = *reinterpret_cast<const float4*>(gr + 2 * (n + i) + 4 * j);
+                                g[2 * j] = w.x; u[2 * j] = w.y; g[2 * j + 1] = w.z; u[2 * j + 1] = w.w;
+                            }
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const float4 w = *reinterpret_cast<const float4*>(gr + n + i + 4 * j);
+                                const float4 x = *reinterpret_cast<const float4*>(gr + a.N + n + i + 4 * j);
+                                g[4 * j] = w.x; g[4 * j + 1] = w.y; g[4 * j + 2] = w.z; g[4 * j + 3] = w.w;
+                                u[4 * j] = x.x; u[4 * j + 1] = x.y; u[4 * j + 2] = x.z; u[4 * j + 3] = x.w;
+                            }
+                        }
+                        float dg[8], du[8], h[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            float hg, hu;
+                            h[j] = gate_slopes(a.gate, g[j], u[j], hg, hu);
+                            const float dh = __uint_as_float(rd[i + j]);
+                            dg[j] = dh * hg;
+                            du[j] = dh * hu;
+                        }
+                        *reinterpret_cast<uint4*>(hr + n + i) = make_uint4(pack_bf16(h[0], h[1]), pack_bf16(h[2], h[3]),
+                                                                           pack_bf16(h[4], h[5]), pack_bf16(h[6], h[7]));
+                        if (a.interleaved) {
+#pragma unroll
+                            for (int j = 0; j < 2; ++j)
+                                *reinterpret_cast<uint4*>(dr + 2 * (n + i) + 8 * j) =
+                                    make_uint4(pack_bf16(dg[4 * j], du[4 * j]), pack_bf16(dg[4 * j + 1], du[4 * j + 1]),
+                                               pack_bf16(dg[4 * j + 2], du[4 * j + 2]), pack_bf16(dg[4 * j + 3], du[4 * j + 3]));
+                        } else {
+                            *reinterpret_cast<uint4*>(dr + n + i) = make_uint4(pack_bf16(dg[0], dg[1]), pack_bf16(dg[2], dg[3]),
+                                                                               pack_bf16(dg[4], dg[5]), pack_bf16(dg[6], dg[7]));
+                            *reinterpret_cast<uint4*>(dr + a.N + n + i) =
+                                make_uint4(pack_bf16(du[0], du[1]), pack_bf16(du[2], du[3]), pack_bf16(du[4], du[5]),
+                                           pack_bf16(du[6], du[7]));
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(map_rank(smem_u32(&acce[acc]), 0));
+            if (++acc == 2) { acc = 0; cph ^= 1u; }
+        }
+    }
+
+    __syncwarp();
+    if (*abort_flag) {  // copies of the abandoned stages land before the memory goes away
+        for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+    }
+    tc_fence_before();
+    cluster_sync_all();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+    }
+}
+
+// MX4 scales [rows, K/32] to the order in which the product copies them:
+// [tile of tr rows][128-k chunk][ceil(tr/128)][32][4] words of four scales, the
+// word of row r (in its tile) and chunk c at lane r % 32, column r / 32 % 4.
+// Rows and scales past the end are 0 (their codes are zero).
+__global__ void __launch_bounds__(256) mx4_tile_scales_kernel(const uint8_t* sa, int64_t rows_a, int tr_a, int tiles_a,
+                                                              uint32_t* oa, const uint8_t* sb, int64_t rows_b,
+                                                              int tr_b, int tiles_b, uint32_t* ob, int64_t pitch,
+                                                              int chunks) {
+    const bool second = blockIdx.y == 1;
+    const uint8_t* s = second ? sb : sa;
+    const int64_t rows = second ? rows_b : rows_a;
+    const int tr = second ? tr_b : tr_a, tiles = second ? tiles_b : tiles_a, subs = (tr + 127) / 128;
+    uint32_t* o = second ? ob : oa;
+    const int groups = (chunks + 3) / 4;  // 16 scales of a row
+    const int64_t total = int64_t(tiles) * subs * 128 * groups;
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < total; i += int64_t(gridDim.x) * 256) {
+        const int64_t pr = i / groups;  // padded row
+        const int g = int(i - pr * groups);
+        const int64_t tile = pr / (subs * 128);
+        const int r = int(pr - tile * subs * 128);
+        const int64_t row = tile * tr + r;
+        uint32_t w[4] = {0, 0, 0, 0};
+        if (r < tr && row < rows) {
+            const uint8_t* p = s + row * pitch;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    const int64_t k = g * 16 + j * 4 + b;
+                    if (k < pitch) w[j] |= uint32_t(p[k]) << (8 * b);
+                }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int c = g * 4 + j;
+            if (c < chunks)
+                o[((tile * chunks + c) * subs + (r >> 7)) * 128 + (r & 31) * 4 + ((r >> 5) & 3)] = w[j];
+        }
+    }
+}
+
+int sm_count() {
+    int dev = 0, sms = 148;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    return sms;
+}
+
+template <bool MX4, bool AMN, bool BMN, int EPI>
+cudaError_t launch_one(const CUtensorMap (&maps)[4], const PairArgs& a, cudaStream_t st) {
+    auto kern = dense_pair_kernel<MX4, AMN, BMN, EPI>;
+    // a per-device attribute: set on every launch (a host-side store)
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PairCfg<MX4>::kSmem);
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = int64_t(a.tiles_m) * a.tiles_n, pairs = sm_count() / 2;
+    const int grid = 2 * int(tiles < pairs ? tiles : pairs);
+    kern<<<grid, kPThreads, PairCfg<MX4>::kSmem, st>>>(maps[0], maps[1], maps[2], maps[3], a);
+    return cudaGetLastError();
+}
+
+// Map of an operand (bf16): 128-byte boxes of `rows` rows along k, or 64 x 64
+// boxes across. `pair` > 0: two row sets (gate, up) as the outer dimension,
+// pair elements apart.
+MapSpec bf16_spec(const DenseOperand& o, int64_t rows, int64_t K, uint32_t box_rows, int64_t pair) {
+    MapSpec s{};
+    s.p = o.p;
+    s.type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    s.swizzle = true;
+    const bool mn = o.k_step != 1;
+    const int64_t line = mn ? o.k_step : o.row;
+    s.dims[0] = uint64_t(mn ? rows : K);
+    s.dims[1] = uint64_t(mn ? K : rows);
+    s.dims[2] = pair ? 2 : 1;
+    s.strides[0] = uint64_t(line) * 2;
+    s.strides[1] = pair ? uint64_t(pair) * 2 : uint64_t(line) * 2;
+    s.box[0] = 64;
+    s.box[1] = mn ? 64 : box_rows;
+    s.box[2] = 1;
+    return s;
+}
+
+int64_t pair_chunks(int64_t K) { return 2 * ((K + 255) / 256); }
+int64_t up256(int64_t v) { return (v + 255) & ~int64_t(255); }
+
+}  // namespace
+
+size_t dense_pair_workspace(int64_t M, int64_t N, int64_t K) {
+    const int64_t c = pair_chunks(K);
+    return size_t(up256(((M + 255) / 256) * 2 * c * 512) + up256(((N + 239) / 240) * c * 1024));
+}
+
+cudaError_t launch_dense_pair(const DenseArgs& d, cudaStream_t st) {
+    const int BN = d.mx4 ? 240 : 256;
+    const bool gate = d.epi == kEpiGate;
+    PairArgs a{};
+    a.M = d.M;
+    a.N = gate ? d.N / 2 : d.N;
+    a.K = d.K;
+    a.tiles_m = int((d.M + 255) / 256);
+    a.tiles_n = int((a.N + (gate ? 128 : BN) - 1) / (gate ? 128 : BN));
+    a.nks = int((d.K + (d.mx4 ? 255 : 63)) / (d.mx4 ? 256 : 64));
+    a.epi = d.epi;
+    a.out_f32 = d.out_f32;
+    a.interleaved = d.interleaved;
+    a.bias = d.bias;
+    a.out = d.out;
+    a.gu = d.gu;
+    a.dgu = d.dgu;
+    a.gate = d.gate;
+    a.status = d.status;
+    a.reset_status = d.reset_status;
+    a.vec_out = (d.N * (d.out_f32 ? 4 : 2)) % 16 == 0 && (reinterpret_cast<uintptr_t>(d.out) & 15) == 0;
+    if (int64_t(a.tiles_m) * a.tiles_n > (int64_t(1) << 30)) return cudaErrorInvalidValue;
+    CUtensorMap maps[4] = {};
+    cudaError_t e;
+    if (d.mx4) {
+        const int64_t c = pair_chunks(d.K), ta = int64_t(a.tiles_m) * 2, tb = a.tiles_n;
+        a.chunks = int(c);
+        uint8_t* oa = (uint8_t*)d.scratch;
+        uint8_t* ob = oa + up256(ta * c * 512);
+        const int64_t words = (ta > 2 * tb ? ta : 2 * tb) * 128 * ((c + 3) / 4);
+        const int64_t blocks = (words + 255) / 256;
+        mx4_tile_scales_kernel<<<dim3(unsigned(blocks < 4096 ? blocks : 4096), 2), 256, 0, st>>>(
+            d.a.s, d.M, 128, int(ta), (uint32_t*)oa, d.b.s, d.N, BN, int(tb), (uint32_t*)ob, d.K / 32, int(c));
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        for (int i = 0; i < 2; ++i) {
+            MapSpec s{};
+            s.p = i ? d.b.p : d.a.p;
+            s.type = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+            s.dims[0] = uint64_t(d.K / 2);
+            s.dims[1] = uint64_t(i ? d.N : d.M);
+            s.dims[2] = 1;
+            s.strides[0] = s.strides[1] = uint64_t(d.K / 2);
+            s.box[0] = 128;
+            s.box[1] = i ? uint32_t(BN / 2) : 128u;
+            s.box[2] = 1;
+            s.swizzle = true;
+            if ((e = encode_map(&maps[i], s)) != cudaSuccess) return e;
+            MapSpec sc{};
+            sc.p = i ? ob : oa;
+            sc.type = CU_TENSOR_MAP_DATA_TYPE_INT32;
+            sc.dims[0] = 256;
+            sc.dims[1] = uint64_t(i ? tb * c : ta * c / 2);
+            sc.dims[2] = 1;
+            sc.strides[0] = sc.strides[1] = 1024;
+            sc.box[0] = 256;
+            sc.box[1] = i ? 2 : 1;
+            sc.box[2] = 1;
+            if ((e = encode_map(&maps[2 + i], sc)) != cudaSuccess) return e;
+        }
+        return launch_one<true, false, false, kEpiStore>(maps, a, st);
+    }
+    if ((e = encode_map(&maps[0], bf16_spec(d.a, d.M, d.K, 128, 0))) != cudaSuccess) return e;
+    if (gate) {  // gate and up rows: every other row, or the two halves
+        DenseOperand w = d.b;
+        if (d.interleaved) w.row *= 2;
+        e = encode_map(&maps[1], bf16_spec(w, a.N, d.K, 128, d.interleaved ? d.b.row : a.N * d.b.row));
+    } else {
+        e = encode_map(&maps[1], bf16_spec(d.b, d.N, d.K, 128, 0));
+    }
+    if (e != cudaSuccess) return e;
+    const bool amn = d.a.k_step != 1, bmn = d.b.k_step != 1;
+    maps[2] = maps[3] = maps[0];
+    if (gate) return launch_one<false, false, false, kEpiGate>(maps, a, st);
+    if (d.epi == kEpiGateBwd) return launch_one<false, false, true, kEpiGateBwd>(maps, a, st);
+    if (amn) return launch_one<false, true, true, kEpiStore>(maps, a, st);
+    return bmn ? launch_one<false, false, true, kEpiStore>(maps, a, st)
+               : launch_one<false, false, false, kEpiStore>(maps, a, st);
+}
+
+}  // namespace qmoe
