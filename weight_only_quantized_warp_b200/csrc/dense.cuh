@@ -116,6 +116,12 @@ struct DenseArgs {
 size_t dense_pair_workspace(int64_t M, int64_t N, int64_t K);  // re-laid MX4 scales
 cudaError_t launch_dense_pair(const DenseArgs& a, cudaStream_t st);
 
+// The same for few rows of A (kEpiStore and kEpiGate, both operands along k):
+// M up to kStreamRows. `after` says that the kernel before it on the stream,
+// which wrote A, may still be running (it triggers programmatic launch).
+constexpr int64_t kStreamRows = 64;
+cudaError_t launch_dense_stream(const DenseArgs& a, bool after, cudaStream_t st);
+
 // out[n] = sum_m x[m, n] (x [M, N] bf16) in a fixed order; part: workspace of
 // colsum_bytes(M, N).
 size_t colsum_bytes(int64_t M, int64_t N);

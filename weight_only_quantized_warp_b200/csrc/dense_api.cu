@@ -118,6 +118,11 @@ struct FfnLayout : Layout {
     }
 };
 
+// Few rows stream the weights, more run on CTA pairs.
+cudaError_t launch_rows(const DenseArgs& a, bool after, cudaStream_t st) {
+    return a.M <= kStreamRows ? launch_dense_stream(a, after, st) : launch_dense_pair(a, st);
+}
+
 DenseOperand rows_of(const void* p, int64_t ld) { return {p, nullptr, ld, 1}; }   // k along the row
 DenseOperand cols_of(const void* p, int64_t ld) { return {p, nullptr, 1, ld}; }   // k across the rows
 
@@ -159,7 +164,7 @@ qmoe_status qmoe_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int
 size_t qmoe_mx4_linear_workspace_size(int64_t T, int64_t N, int64_t K) {
     if (T < 0 || N < 1 || K < 32 || K % 32 || T > kMaxDim || N > kMaxDim || K > kMaxDim) return 0;
     Layout l;
-    l.take(dense_pair_workspace(T, N, K));
+    if (T > kStreamRows) l.take(dense_pair_workspace(T, N, K));
     return l.total;
 }
 
@@ -195,7 +200,7 @@ qmoe_status qmoe_mx4_linear(int64_t T, int64_t N, int64_t K, const uint8_t* x_co
     a.status = (int32_t*)workspace;
     a.reset_status = 1;
     a.scratch = (char*)workspace + Layout().total;
-    const cudaError_t e = launch_dense_pair(a, (cudaStream_t)stream);
+    const cudaError_t e = launch_rows(a, false, (cudaStream_t)stream);
     return e == cudaSuccess ? QMOE_OK : cuda_bad(e, "mx4_linear");
 }
 
@@ -234,7 +239,7 @@ qmoe_status qmoe_gated_ffn_forward(const qmoe_gated_ffn_config* cfg, int64_t T, 
     a.interleaved = cfg->swiglu_fusion == 1;
     a.status = (int32_t*)workspace;
     a.reset_status = 1;
-    cudaError_t e = launch_dense_pair(a, st);
+    cudaError_t e = launch_rows(a, false, st);
     DenseArgs d{};
     d.a = rows_of(h, I);
     d.b = rows_of(w2, I);
@@ -245,7 +250,7 @@ qmoe_status qmoe_gated_ffn_forward(const qmoe_gated_ffn_config* cfg, int64_t T, 
     d.bias = b2;
     d.out = y;
     d.status = (int32_t*)workspace;
-    if (e == cudaSuccess) e = launch_dense_pair(d, st);
+    if (e == cudaSuccess) e = launch_rows(d, true, st);
     return e == cudaSuccess ? QMOE_OK : cuda_bad(e, "gated_ffn_forward");
 }
 

@@ -401,16 +401,7 @@ __global__ void __launch_bounds__(256) mx4_tile_scales_kernel(const uint8_t* sa,
         const int r = int(pr - tile * subs * 128);
         const int64_t row = tile * tr + r;
         uint32_t w[4] = {0, 0, 0, 0};
-        if (r < tr && row < rows) {
-            const uint8_t* p = s + row * pitch;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    const int64_t k = g * 16 + j * 4 + b;
-                    if (k < pitch) w[j] |= uint32_t(p[k]) << (8 * b);
-                }
-        }
+        if (r < tr && row < rows) load_scales<4>(s, rows * pitch, row, pitch, g * 16, w);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int c = g * 4 + j;
@@ -420,44 +411,15 @@ __global__ void __launch_bounds__(256) mx4_tile_scales_kernel(const uint8_t* sa,
     }
 }
 
-int sm_count() {
-    int dev = 0, sms = 148;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    return sms;
-}
-
 template <bool MX4, bool AMN, bool BMN, int EPI>
 cudaError_t launch_one(const CUtensorMap (&maps)[4], const PairArgs& a, cudaStream_t st) {
-    auto kern = dense_pair_kernel<MX4, AMN, BMN, EPI>;
-    // a per-device attribute: set on every launch (a host-side store)
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PairCfg<MX4>::kSmem);
+    constexpr auto kern = dense_pair_kernel<MX4, AMN, BMN, EPI>;
+    cudaError_t e = raise_smem<kern>(PairCfg<MX4>::kSmem);
     if (e != cudaSuccess) return e;
     const int64_t tiles = int64_t(a.tiles_m) * a.tiles_n, pairs = sm_count() / 2;
     const int grid = 2 * int(tiles < pairs ? tiles : pairs);
     kern<<<grid, kPThreads, PairCfg<MX4>::kSmem, st>>>(maps[0], maps[1], maps[2], maps[3], a);
     return cudaGetLastError();
-}
-
-// Map of an operand (bf16): 128-byte boxes of `rows` rows along k, or 64 x 64
-// boxes across. `pair` > 0: two row sets (gate, up) as the outer dimension,
-// pair elements apart.
-MapSpec bf16_spec(const DenseOperand& o, int64_t rows, int64_t K, uint32_t box_rows, int64_t pair) {
-    MapSpec s{};
-    s.p = o.p;
-    s.type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    s.swizzle = true;
-    const bool mn = o.k_step != 1;
-    const int64_t line = mn ? o.k_step : o.row;
-    s.dims[0] = uint64_t(mn ? rows : K);
-    s.dims[1] = uint64_t(mn ? K : rows);
-    s.dims[2] = pair ? 2 : 1;
-    s.strides[0] = uint64_t(line) * 2;
-    s.strides[1] = pair ? uint64_t(pair) * 2 : uint64_t(line) * 2;
-    s.box[0] = 64;
-    s.box[1] = mn ? 64 : box_rows;
-    s.box[2] = 1;
-    return s;
 }
 
 int64_t pair_chunks(int64_t K) { return 2 * ((K + 255) / 256); }
@@ -505,17 +467,7 @@ cudaError_t launch_dense_pair(const DenseArgs& d, cudaStream_t st) {
             d.a.s, d.M, 128, int(ta), (uint32_t*)oa, d.b.s, d.N, BN, int(tb), (uint32_t*)ob, d.K / 32, int(c));
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         for (int i = 0; i < 2; ++i) {
-            MapSpec s{};
-            s.p = i ? d.b.p : d.a.p;
-            s.type = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-            s.dims[0] = uint64_t(d.K / 2);
-            s.dims[1] = uint64_t(i ? d.N : d.M);
-            s.dims[2] = 1;
-            s.strides[0] = s.strides[1] = uint64_t(d.K / 2);
-            s.box[0] = 128;
-            s.box[1] = i ? uint32_t(BN / 2) : 128u;
-            s.box[2] = 1;
-            s.swizzle = true;
+            const MapSpec s = i ? mx4_spec(d.b.p, d.N, d.K, uint32_t(BN / 2)) : mx4_spec(d.a.p, d.M, d.K, 128);
             if ((e = encode_map(&maps[i], s)) != cudaSuccess) return e;
             MapSpec sc{};
             sc.p = i ? ob : oa;

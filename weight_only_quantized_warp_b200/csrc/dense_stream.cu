@@ -1,0 +1,367 @@
+// dense_stream.cu -- the dense operators' products for few tokens (sm_100a).
+//
+// D[t, n] = sum_k X(t, k) W(n, k) for T <= 64 rows of X: bound by reading W
+// once. W's rows are the MMA's M (128 of them, or 128 gate and 128 up rows as
+// two accumulators) and the tokens its N, padded to NT = 16, 32 or 64, so
+// the tensor core takes both operands as they lie (MX4 codes undecoded) and
+// the CTA does nothing per weight but move it: TMA fills a ring of 128-byte
+// wide stages that an MMA warp empties.
+//
+// K is split over the CTAs of a cluster so that about two CTAs per SM stream
+// at once; their fp32 partials meet in shared memory and are added in rank
+// order through distributed shared memory (rank r finishes tokens r, r + S,
+// ...), so the result is the same on every call and there is no second launch.
+//
+// MX4 scales are read where they lie: 128 threads (the later epilogue) take 32
+// scales of a W row and of an X row at a time, four stages' worth, and place
+// them for tcgen05.cp.
+//
+// Warps (192 threads): 0 TMA, 1 MMA and tensor memory, 2-5 scales and
+// epilogue. Every wait is bounded (QMOE_TIMEOUT in the status word).
+#include "dense_tc.cuh"
+
+namespace qmoe {
+namespace {
+
+constexpr int kSThreads = 192;
+constexpr int kSW = 128 * 128;  // W rows of a stage, one accumulator
+
+struct StreamArgs {
+    int64_t N, K, I;  // N: rows of W per accumulator (h columns for the gate)
+    int T, nks, splits;
+    int out_f32, interleaved, after;
+    const uint8_t *ws, *xs;  // MX4 scales
+    const void* bias;
+    void* out;
+    float* gu;
+    GateParams gate;
+    int32_t* status;
+    int reset_status;
+};
+
+template <bool MX4, bool GATE, int NT>
+struct StreamCfg {
+    static constexpr int kX = NT * 128;
+    static constexpr int kS = MX4 ? 2048 : 0;  // W and X scales, 2 x 512 each
+    static constexpr int kStage = kSW * (GATE ? 2 : 1) + kX + kS;
+    static constexpr int kStages = (GATE ? 102 : 106) * 1024 / kStage;
+    static constexpr int kPart = NT * 128 * 4 * (GATE ? 2 : 1);  // partials, over the ring once it has drained
+    static constexpr int kRing = kStages * kStage > kPart ? kStages * kStage : kPart;
+    static constexpr int kSmem = kRing + 1024 + 1024;
+    static constexpr int kAcc = NT * (GATE ? 2 : 1);
+    static constexpr int kWant = kAcc + (MX4 ? 16 : 0);
+    static constexpr int kCols = kWant <= 32 ? 32 : kWant <= 64 ? 64 : 128;
+    static_assert(kStages >= 2 && kStage % 1024 == 0 && kSmem <= 113 * 1024, "two CTAs per SM");
+};
+
+// The results of W row n for token t.
+template <bool GATE>
+__device__ __forceinline__ void stream_emit(const StreamArgs& a, int t, int64_t n, float g, float u, float bg, float bu) {
+    if (GATE) {
+        g += bg;
+        u += bu;
+        if (a.gu) {
+            float* r = a.gu + int64_t(t) * 2 * a.N;
+            r[a.interleaved ? 2 * n : n] = g;
+            r[a.interleaved ? 2 * n + 1 : a.N + n] = u;
+        }
+        reinterpret_cast<__nv_bfloat16*>(a.out)[t * a.N + n] = __float2bfloat16_rn(gate_value(a.gate, g, u));
+    } else if (a.out_f32) {
+        reinterpret_cast<float*>(a.out)[t * a.N + n] = g + bg;
+    } else {
+        reinterpret_cast<__nv_bfloat16*>(a.out)[t * a.N + n] = __float2bfloat16_rn(g + bg);
+    }
+}
+
+template <bool MX4, bool GATE, int NT>
+__global__ void __launch_bounds__(kSThreads, 2)
+    dense_stream_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
+                        const StreamArgs a) {
+    using C = StreamCfg<MX4, GATE, NT>;
+    constexpr int ST = C::kStages, KE = MX4 ? 128 : 64;  // map elements of a stage along k
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = a.splits > 1 ? int(cluster_rank()) : 0;
+    const int n0 = int(blockIdx.x / a.splits) * 128;
+    const int ks0 = int(int64_t(rank) * a.nks / a.splits), ks1 = int(int64_t(rank + 1) * a.nks / a.splits);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kRing);
+    uint64_t* empty = full + ST;
+    uint64_t* accf = empty + ST;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accf + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    if (tid == 0) {
+        for (int s = 0; s < ST; ++s) {
+            mbar_init(smem_u32(&full[s]), MX4 ? 5 : 1);
+            mbar_init(smem_u32(&empty[s]), 1);
+        }
+        mbar_init(smem_u32(accf), 1);
+        *abort_flag = 0;
+        if (a.reset_status && blockIdx.x == 0) *a.status = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "r"(C::kCols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_trigger();
+
+    if (warp == 0) {
+        // ------------------------------------------------------- producer
+        const uint32_t e = elect_one();
+        int st = 0;
+        uint32_t ph = 0;
+        const int first = min(ST, ks1 - ks0);
+        auto load_w = [&](int ks, int s) {
+            const uint32_t sw = smem_u32(smem + s * C::kStage), fb = smem_u32(&full[s]);
+            mbar_expect_tx_e(fb, C::kStage - C::kS, e);
+            tma_3d_e(sw, &wmap, ks * KE, n0, 0, fb, e);
+            if (GATE) tma_3d_e(sw + kSW, &wmap, ks * KE, n0, 1, fb, e);
+        };
+        auto load_x = [&](int ks, int s) {
+            tma_3d_e(smem_u32(smem + s * C::kStage) + kSW * (GATE ? 2 : 1), &xmap, ks * KE, 0, 0, smem_u32(&full[s]), e);
+        };
+        // W does not depend on the kernel before this one: the ring fills
+        // with it first
+        for (int i = 0; i < first; ++i) load_w(ks0 + i, i);
+        if (a.after) pdl_wait();
+        for (int i = 0; i < first; ++i) load_x(ks0 + i, i);
+        for (int ks = ks0 + first; ks < ks1; ++ks) {
+            if (!warp_wait(smem_u32(&empty[st]), ph, abort_flag, a.status, kTimeoutNs)) break;
+            load_w(ks, st);
+            load_x(ks, st);
+            if (++st == ST) { st = 0; ph ^= 1u; }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------- MMA issue
+        const uint32_t e = elect_one();
+        int st = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        const uint32_t ts = tmem + C::kAcc;  // scales: W chunk 0, 1, X chunk 0, 1 (4 columns each)
+        for (int ks = ks0; ks < ks1; ++ks) {
+            if (!warp_wait(smem_u32(&full[st]), ph, abort_flag, a.status, kTimeoutNs)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t sw = smem_u32(smem + st * C::kStage), sx = sw + kSW * (GATE ? 2 : 1);
+            const uint64_t wd = desc_sw128(sw), xd = desc_sw128(sx);
+            const uint32_t acc0 = ks > ks0 ? 1u : 0u;
+            if constexpr (MX4) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) cp_scales_e(ts + 4 * j, desc_scales(sx + C::kX + 512 * j), e);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_mx4_e(tmem, wd + uint64_t(2 * kk), xd + uint64_t(2 * kk), idesc_mx4(128, NT, 2 * (kk & 1)),
+                              ts + 4 * (kk >> 1), ts + 8 + 4 * (kk >> 1), kk > 0 ? 1u : acc0, e);
+            } else {
+                constexpr uint32_t id = idesc_f16(128, NT, false, false);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                    const uint32_t acc = kk > 0 ? 1u : acc0;
+                    mma_bf16_ss_e(tmem, wd + uint64_t(2 * kk), xd + uint64_t(2 * kk), id, acc, e);
+                    if (GATE)
+                        mma_bf16_ss_e(tmem + NT, desc_sw128(sw + kSW) + uint64_t(2 * kk), xd + uint64_t(2 * kk), id, acc, e);
+                }
+            }
+            mma_commit_e(smem_u32(&empty[st]), e);
+            if (++st == ST) { st = 0; ph ^= 1u; }
+        }
+        if (ok) mma_commit_e(smem_u32(accf), e);
+    } else {
+        const int et = tid - 64;  // 0 .. 127
+        bool ok = true;
+        if constexpr (MX4) {
+            // ------------------------------------------- scales: row et of W and X
+            if (a.after) pdl_wait();
+            const int64_t pitch = a.K / 32, nw = n0 + et;
+            int st = 0;
+            uint32_t ph = 0;
+            uint32_t w[8], x[8];
+            auto fetch = [&](int ks) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j] = x[j] = 0;
+                if (ks >= ks1) return;
+                if (nw < a.N) load_scales<8>(a.ws, a.N * pitch, nw, pitch, int64_t(ks) * 8, w);
+                if (et < a.T) load_scales<8>(a.xs, int64_t(a.T) * pitch, et, pitch, int64_t(ks) * 8, x);
+            };
+            fetch(ks0);
+            for (int ks = ks0; ok && ks < ks1; ks += 4) {
+                uint32_t cw[8], cx[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) { cw[j] = w[j]; cx[j] = x[j]; }
+                fetch(ks + 4);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (ks + i >= ks1) break;
+                    if (!warp_wait(smem_u32(&empty[st]), ph ^ 1u, abort_flag, a.status, kTimeoutNs)) { ok = false; break; }
+                    uint32_t* sc = reinterpret_cast<uint32_t*>(smem + st * C::kStage + kSW + C::kX) + (et & 31) * 4 + (et >> 5);
+                    sc[0] = cw[2 * i];
+                    sc[128] = cw[2 * i + 1];
+                    if (et < NT) {
+                        sc[256] = cx[2 * i];
+                        sc[384] = cx[2 * i + 1];
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&full[st]));
+                    if (++st == ST) { st = 0; ph ^= 1u; }
+                }
+            }
+        }
+        // ------------------------------------------------------- epilogue
+        ok = ok && warp_wait(smem_u32(accf), 0, abort_flag, a.status, kTimeoutNs);
+        tc_fence_after();
+        const int row = (warp & 3) * 32 + lane;
+        const int64_t n = n0 + row;
+        const bool valid = n < a.N;
+        const uint32_t tb = tmem + (uint32_t((warp & 3) * 32) << 16);
+        const bool some = ks1 > ks0;  // an empty split has no accumulator
+        float bg = 0.0f, bu = 0.0f;
+        if (a.bias && valid) {
+            if (GATE) {
+                const __nv_bfloat16* b = reinterpret_cast<const __nv_bfloat16*>(a.bias);
+                bg = __bfloat162float(b[a.interleaved ? 2 * n : n]);
+                bu = __bfloat162float(b[a.interleaved ? 2 * n + 1 : a.N + n]);
+            } else {
+                bg = a.out_f32 ? reinterpret_cast<const float*>(a.bias)[n]
+                               : __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(a.bias)[n]);
+            }
+        }
+        float* part = reinterpret_cast<float*>(smem);  // [accumulator][token][128]
+        // the output (and, when this is the call's second product, its inputs'
+        // buffer) may still be in use by the kernel before
+        if (a.after) pdl_wait();
+        if (ok) {
+            for (int t0 = 0; t0 < a.T; t0 += 16) {
+                float v[16], u[16];
+                tmem_ld16(tb + uint32_t(t0), v);
+                if (GATE) tmem_ld16(tb + uint32_t(NT + t0), u);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    if (t0 + j >= a.T) break;
+                    const float g = some ? v[j] : 0.0f, up = GATE && some ? u[j] : 0.0f;
+                    if (a.splits > 1) {
+                        part[(t0 + j) * 128 + row] = g;
+                        if (GATE) part[(NT + t0 + j) * 128 + row] = up;
+                    } else if (valid) {
+                        stream_emit<GATE>(a, t0 + j, n, g, up, bg, bu);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        if (a.splits > 1) {
+            cluster_sync_all();
+            if (valid) {
+                const uint32_t base = smem_u32(part) + row * 4;
+                for (int t = rank; t < a.T; t += a.splits) {
+                    float g = 0.0f, u = 0.0f;
+                    for (int s = 0; s < a.splits; ++s) {
+                        g += ld_cluster_f32(map_rank(base + t * 512, s));
+                        if (GATE) u += ld_cluster_f32(map_rank(base + (NT + t) * 512, s));
+                    }
+                    stream_emit<GATE>(a, t, n, g, u, bg, bu);
+                }
+            }
+        }
+    }
+    if (a.splits > 1 && warp < 2) cluster_sync_all();
+    __syncwarp();
+    if (*abort_flag) {  // copies of the abandoned stages land before the memory goes away
+        for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+    }
+    tc_fence_before();
+    if (a.splits > 1) cluster_sync_all();  // nobody leaves while its partials are read
+    else __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols));
+    }
+}
+
+template <bool MX4, bool GATE, int NT>
+cudaError_t launch_nt(const CUtensorMap& wmap, const CUtensorMap& xmap, const StreamArgs& a, int tiles, cudaStream_t st) {
+    constexpr auto kern = dense_stream_kernel<MX4, GATE, NT>;
+    using C = StreamCfg<MX4, GATE, NT>;
+    cudaError_t e = raise_smem<kern>(C::kSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(tiles * a.splits));
+    cfg.blockDim = dim3(kSThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (a.splits > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = unsigned(a.splits);
+        attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    if (a.after) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n].val.programmaticStreamSerializationAllowed = 1;
+        ++n;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = unsigned(n);
+    return cudaLaunchKernelEx(&cfg, kern, wmap, xmap, a);
+}
+
+template <bool MX4, bool GATE>
+cudaError_t launch_any(const CUtensorMap& wmap, const CUtensorMap& xmap, const StreamArgs& a, int tiles, cudaStream_t st) {
+    if (a.T <= 16) return launch_nt<MX4, GATE, 16>(wmap, xmap, a, tiles, st);
+    if (a.T <= 32) return launch_nt<MX4, GATE, 32>(wmap, xmap, a, tiles, st);
+    return launch_nt<MX4, GATE, 64>(wmap, xmap, a, tiles, st);
+}
+
+}  // namespace
+
+cudaError_t launch_dense_stream(const DenseArgs& d, bool after, cudaStream_t st) {
+    const bool gate = d.epi == kEpiGate;
+    StreamArgs a{};
+    a.T = int(d.M);
+    a.N = gate ? d.N / 2 : d.N;
+    a.K = d.K;
+    a.nks = int((d.K + (d.mx4 ? 255 : 63)) / (d.mx4 ? 256 : 64));
+    a.out_f32 = d.out_f32;
+    a.interleaved = d.interleaved;
+    a.after = after;
+    a.ws = d.b.s;
+    a.xs = d.a.s;
+    a.bias = d.bias;
+    a.out = d.out;
+    a.gu = d.gu;
+    a.gate = d.gate;
+    a.status = d.status;
+    a.reset_status = d.reset_status;
+    const int64_t tiles = (a.N + 127) / 128;
+    // Splits of K: as many (a cluster holds 8) as keep all CTAs resident, two
+    // per SM, and every split at least two stages long.
+    const int64_t slots = 2 * sm_count();
+    a.splits = 1;
+    while (a.splits < 8 && tiles * (a.splits + 1) <= slots && a.nks >= 2 * (a.splits + 1)) ++a.splits;
+    if (tiles * a.splits > (int64_t(1) << 30)) return cudaErrorInvalidValue;
+    const uint32_t nt = d.M <= 16 ? 16 : d.M <= 32 ? 32 : 64;
+    CUtensorMap wmap, xmap;
+    cudaError_t e;
+    if (d.mx4) {
+        if ((e = encode_map(&wmap, mx4_spec(d.b.p, d.N, d.K, 128))) != cudaSuccess) return e;
+        if ((e = encode_map(&xmap, mx4_spec(d.a.p, d.M, d.K, nt))) != cudaSuccess) return e;
+        return launch_any<true, false>(wmap, xmap, a, int(tiles), st);
+    }
+    if ((e = encode_map(&xmap, bf16_spec(d.a, d.M, d.K, nt, 0))) != cudaSuccess) return e;
+    DenseOperand w = d.b;
+    if (gate && d.interleaved) w.row *= 2;
+    e = encode_map(&wmap, bf16_spec(w, a.N, d.K, 128, !gate ? 0 : d.interleaved ? d.b.row : a.N * d.b.row));
+    if (e != cudaSuccess) return e;
+    return gate ? launch_any<false, true>(wmap, xmap, a, int(tiles), st)
+                : launch_any<false, false>(wmap, xmap, a, int(tiles), st);
+}
+
+}  // namespace qmoe

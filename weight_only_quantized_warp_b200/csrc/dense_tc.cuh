@@ -3,6 +3,8 @@
 // majors and for 4-bit blocks, tensor maps and the epilogues' arithmetic.
 #pragma once
 
+#include <atomic>
+
 #include "dense.cuh"
 #include "tc_common.cuh"
 
@@ -102,6 +104,69 @@ __device__ __forceinline__ void cp_scales_pair_e(uint32_t t, uint64_t sdesc, uin
         : "memory");
 }
 
+// The one-CTA forms.
+__device__ __forceinline__ void mma_mx4_e(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t sa,
+                                          uint32_t sb, uint32_t acc, uint32_t e) {
+    asm volatile(
+        "{\n.reg .pred p, q;\nsetp.ne.b32 p, %6, 0;\nsetp.ne.b32 q, %7, 0;\n"
+        "@q tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),
+        "l"(ad), "l"(bd), "r"(idesc), "r"(sa), "r"(sb), "r"(acc), "r"(e));
+}
+__device__ __forceinline__ void cp_scales_e(uint32_t t, uint64_t sdesc, uint32_t e) {
+    asm volatile(
+        "{\n.reg .pred q;\nsetp.ne.b32 q, %2, 0;\n@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n}" ::"r"(t),
+        "l"(sdesc), "r"(e)
+        : "memory");
+}
+// A float of another CTA's shared memory (cluster address).
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// 4 NW consecutive scales of a row of `pitch` scales, from scale k0 on (a
+// multiple of 4), as words; 0 past the row's end. The array starts on 4 bytes
+// and holds `total` of them; rows need not be aligned, so a row's words are
+// joined from the aligned words that hold them.
+template <int NW>
+__device__ __forceinline__ void load_scales(const uint8_t* s, int64_t total, int64_t row, int64_t pitch, int64_t k0,
+                                            uint32_t (&w)[NW]) {
+    const int64_t at = row * pitch + k0;
+    const int n = int(min(int64_t(4 * NW), max(int64_t(0), pitch - k0)));  // bytes of the row
+    if (NW % 4 == 0 && ((pitch | reinterpret_cast<uintptr_t>(s)) & 15) == 0 && (k0 & 15) == 0) {
+#pragma unroll
+        for (int j = 0; j < NW / 4; ++j) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (16 * j < n) v = __ldg(reinterpret_cast<const uint4*>(s + at) + j);
+            w[4 * j] = v.x; w[4 * j + 1] = v.y; w[4 * j + 2] = v.z; w[4 * j + 3] = v.w;
+        }
+        return;
+    }
+    const int sh = int(at & 3);
+    const int64_t a0 = at - sh;
+    uint32_t r[NW + 1];
+#pragma unroll
+    for (int j = 0; j <= NW; ++j) {
+        const int64_t p = a0 + 4 * j;
+        r[j] = 0;
+        if (4 * j < n + sh) {
+            if (p + 4 <= total) {
+                r[j] = __ldg(reinterpret_cast<const uint32_t*>(s + p));
+            } else {  // the array's last bytes
+                for (int b = 0; b < 4; ++b)
+                    if (p + b < total) r[j] |= uint32_t(s[p + b]) << (8 * b);
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < NW; ++j) {
+        w[j] = __funnelshift_r(r[j], r[j + 1], 8 * sh);
+        const int left = n - 4 * j;
+        if (left < 4) w[j] &= left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+    }
+}
+
 // Shared-memory descriptor of an operand whose rows (M or N) lie along
 // 128-byte swizzled lines of 64 bf16, one line per k: 64-row chunks 8192 bytes
 // apart (64 k each), groups of 8 k 1024 bytes apart.
@@ -155,6 +220,25 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 
 // ---------------------------------------------------------------- host side
 
+inline int sm_count() {
+    int dev = 0, sms = 148;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    return sms;
+}
+
+// Raise a kernel's shared-memory limit, once per device.
+template <auto Kern>
+inline cudaError_t raise_smem(int bytes) {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && (done.load(std::memory_order_acquire) >> dev & 1))) return e;
+    e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64) done.fetch_or(uint64_t(1) << dev, std::memory_order_release);
+    return e;
+}
+
 // Tensor map of up to three dimensions with 128-byte swizzled boxes (or
 // plain ones): dims and boxes in elements, strides of the outer two in bytes.
 struct MapSpec {
@@ -175,6 +259,43 @@ inline cudaError_t encode_map(CUtensorMap* map, const MapSpec& s) {
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? cudaSuccess
                : cudaErrorInvalidValue;
+}
+
+// Map of an operand (bf16): 128-byte boxes of `rows` rows along k, or 64 x 64
+// boxes across. `pair` > 0: two row sets (gate, up) as the outer dimension,
+// pair elements apart.
+inline MapSpec bf16_spec(const DenseOperand& o, int64_t rows, int64_t K, uint32_t box_rows, int64_t pair) {
+    MapSpec s{};
+    s.p = o.p;
+    s.type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    s.swizzle = true;
+    const bool mn = o.k_step != 1;
+    const int64_t line = mn ? o.k_step : o.row;
+    s.dims[0] = uint64_t(mn ? rows : K);
+    s.dims[1] = uint64_t(mn ? K : rows);
+    s.dims[2] = pair ? 2 : 1;
+    s.strides[0] = uint64_t(line) * 2;
+    s.strides[1] = pair ? uint64_t(pair) * 2 : uint64_t(line) * 2;
+    s.box[0] = 64;
+    s.box[1] = mn ? 64 : box_rows;
+    s.box[2] = 1;
+    return s;
+}
+
+// Map of MX4 codes: 128-byte boxes (256 k) of `box_rows` rows.
+inline MapSpec mx4_spec(const void* codes, int64_t rows, int64_t K, uint32_t box_rows) {
+    MapSpec s{};
+    s.p = codes;
+    s.type = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    s.dims[0] = uint64_t(K / 2);
+    s.dims[1] = uint64_t(rows);
+    s.dims[2] = 1;
+    s.strides[0] = s.strides[1] = uint64_t(K / 2);
+    s.box[0] = 128;
+    s.box[1] = box_rows;
+    s.box[2] = 1;
+    s.swizzle = true;
+    return s;
 }
 
 }  // namespace

@@ -14,6 +14,7 @@ torch's allocator, so calls on several streams and captured graphs share none.
 """
 from __future__ import annotations
 
+import ctypes
 from typing import NamedTuple, Optional
 
 import torch
@@ -25,74 +26,89 @@ MX4_BLOCK = 32
 
 
 def _dtype_code(dtype) -> int:
-    if dtype not in _DTYPES:
+    code = _DTYPES.get(dtype)
+    if code is None:
         raise ValueError(f"dtype must be float32 or bfloat16, not {dtype}")
-    return _DTYPES[dtype]
+    return code
 
 
-def _need(cond, text):
-    if not cond:
-        raise ValueError(text)
+def _tensor(t, name, shape, dtype, index):
+    """Check an operand: a contiguous tensor of this shape and type on GPU ``index``."""
+    if t.shape != shape or t.dtype != dtype or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on GPU {index}, "
+                         f"not {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
 
 
-def _tensor(t, name, shape, dtype, device):
-    """Check an operand: a contiguous tensor of this shape, type and device."""
-    _need(t.shape == shape, f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    _need(t.dtype == dtype, f"{name} must be {dtype}, not {t.dtype}")
-    _need(t.device == device, f"{name} is on {t.device}, not on {device}")
-    _need(t.is_contiguous(), f"{name} must be contiguous")
+def _gpu(t, name) -> int:
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name} must be on a GPU, not on {t.device}")
+    return index
 
 
-def _workspace(n, device):
-    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+def _enqueue(index, call, *args):
+    """``call(*args, stream)`` on GPU ``index``, on torch's current stream of it."""
+    if torch.cuda.current_device() == index:
+        status = call(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            status = call(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status:
+        raise qmoe.QMoEError(status, qmoe.lib.qmoe_dense_last_error().decode())
 
 
-def _rows(x):
-    """x as (tensor, rows, K, row stride): a 2-D tensor with unit stride along
-    K is taken as it lies, any other one through a contiguous copy."""
-    if x.dim() != 2:
-        x = x.reshape(-1, x.shape[-1])
-    rows, K = x.shape
-    es = x.element_size()
-    if K and not (x.stride(1) == 1 and x.data_ptr() % 16 == 0
-                  and (rows <= 1 or (x.stride(0) >= K and x.stride(0) * es % 16 == 0))):
-        x = x.clone(memory_format=torch.contiguous_format)
-    return x, rows, K, (x.stride(0) if rows > 1 else K)
+def _address(t):
+    return None if t is None else t.data_ptr()
 
 
 def mx4_quantize(x):
     """x [..., K] (float32 or bfloat16, K a multiple of 32) to ``(codes, scales)``:
-    uint8 [..., K/2] and [..., K/32]."""
+    uint8 [..., K/2] and [..., K/32]. A 2-D x with unit stride along K and
+    16-byte aligned rows is read where it lies, any other layout through a
+    contiguous copy."""
     code = _dtype_code(x.dtype)
-    _need(x.dim() >= 1 and x.shape[-1] > 0 and x.shape[-1] % MX4_BLOCK == 0,
-          f"the last dimension must be a positive multiple of {MX4_BLOCK}")
-    lead = x.shape[:-1]
-    with torch.cuda.device(x.device):
-        x, rows, K, ldx = _rows(x)
-        codes = torch.empty(*lead, K // 2, dtype=torch.uint8, device=x.device)
-        scales = torch.empty(*lead, K // MX4_BLOCK, dtype=torch.uint8, device=x.device)
-        if rows:
-            qmoe.qmoe_mx4_quantize(x.data_ptr(), code, rows, K, ldx, codes, scales)
+    shape = x.shape
+    if not shape or shape[-1] < MX4_BLOCK or shape[-1] % MX4_BLOCK:
+        raise ValueError(f"the last dimension must be a positive multiple of {MX4_BLOCK}")
+    index, K = _gpu(x, "x"), shape[-1]
+    ldx = K
+    if not x.is_contiguous():
+        if x.dim() == 2 and x.stride(1) == 1 and x.stride(0) >= K and x.stride(0) * x.element_size() % 16 == 0:
+            ldx = x.stride(0)
+        else:
+            x = x.contiguous()
+    if x.data_ptr() % 16:
+        x, ldx = x.clone(memory_format=torch.contiguous_format), K
+    lead = shape[:-1]
+    codes = x.new_empty((*lead, K // 2), dtype=torch.uint8)
+    scales = x.new_empty((*lead, K // MX4_BLOCK), dtype=torch.uint8)
+    rows = x.numel() // K
+    if rows:
+        _enqueue(index, qmoe.lib.qmoe_mx4_quantize, x.data_ptr(), code, rows, K, ldx, codes.data_ptr(),
+                 scales.data_ptr())
     return codes, scales
 
 
-def _check_mx4(codes, scales, name):
-    _need(codes.dtype == torch.uint8 and scales.dtype == torch.uint8, f"{name}codes and {name}scales must be uint8")
-    _need(codes.dim() >= 1 and codes.shape[-1] > 0 and codes.shape[-1] % (MX4_BLOCK // 2) == 0,
-          f"{name}codes must hold a positive multiple of {MX4_BLOCK} per row")
-    _tensor(scales, f"{name}scales", (*codes.shape[:-1], codes.shape[-1] * 2 // MX4_BLOCK), torch.uint8, codes.device)
-    _need(codes.is_contiguous(), f"{name}codes must be contiguous")
+def _check_mx4(codes, scales, name) -> int:
+    """Check MX4 rows; their length K."""
+    c = codes.shape
+    if not c or c[-1] < MX4_BLOCK // 2 or c[-1] % (MX4_BLOCK // 2):
+        raise ValueError(f"{name}codes must hold a positive multiple of {MX4_BLOCK} per row")
+    index = codes.get_device()
+    _tensor(codes, name + "codes", c, torch.uint8, index)
+    _tensor(scales, name + "scales", (*c[:-1], c[-1] // (MX4_BLOCK // 2)), torch.uint8, index)
+    return c[-1] * 2
 
 
 def mx4_dequantize(codes, scales, dtype=torch.bfloat16):
     """The values of MX4 rows, [..., K] of ``dtype``."""
     code = _dtype_code(dtype)
-    _check_mx4(codes, scales, "")
-    K = codes.shape[-1] * 2
-    with torch.cuda.device(codes.device):
-        x = torch.empty(*codes.shape[:-1], K, dtype=dtype, device=codes.device)
-        if x.numel():
-            qmoe.qmoe_mx4_dequantize(codes, scales, x.numel() // K, K, x, code, K)
+    K = _check_mx4(codes, scales, "")
+    index = _gpu(codes, "codes")
+    x = codes.new_empty((*codes.shape[:-1], K), dtype=dtype)
+    rows = x.numel() // K
+    if rows:
+        _enqueue(index, qmoe.lib.qmoe_mx4_dequantize, codes.data_ptr(), scales.data_ptr(), rows, K, x.data_ptr(), code, K)
     return x
 
 
@@ -100,22 +116,22 @@ def mx4_linear(x_codes, x_scales, w_codes, w_scales, bias=None, dtype=torch.bflo
     """y [..., N] = deq(x) deq(w)^T + bias for MX4 rows x [..., K] and w [N, K];
     bias and y are ``dtype``."""
     code = _dtype_code(dtype)
-    _check_mx4(x_codes, x_scales, "x_")
-    _check_mx4(w_codes, w_scales, "w_")
-    dev = x_codes.device
-    _need(w_codes.dim() == 2 and w_codes.shape[0] > 0, "w_codes must be [N, K/2]")
-    _need(w_codes.shape[1] == x_codes.shape[-1], "x and w rows differ in length")
-    _need(w_codes.device == dev, "x and w are on different devices")
-    N, K = w_codes.shape[0], w_codes.shape[1] * 2
+    K = _check_mx4(x_codes, x_scales, "x_")
+    if _check_mx4(w_codes, w_scales, "w_") != K or w_codes.dim() != 2 or not w_codes.shape[0]:
+        raise ValueError(f"w_codes must be [N, K/2] with x's row length {K}, not {tuple(w_codes.shape)}")
+    index, N = x_codes.get_device(), w_codes.shape[0]
+    if w_codes.get_device() != index:
+        raise ValueError(f"x is on {x_codes.device}, w on {w_codes.device}")
     if bias is not None:
-        _tensor(bias, "bias", (N,), dtype, dev)
-    with torch.cuda.device(dev):
-        y = torch.empty(*x_codes.shape[:-1], N, dtype=dtype, device=dev)
-        T = y.numel() // N
-        if T:
-            n = qmoe.qmoe_mx4_linear_workspace_size(T, N, K)
-            ws = _workspace(n, dev)
-            qmoe.qmoe_mx4_linear(T, N, K, x_codes, x_scales, w_codes, w_scales, bias, y, code, ws, n)
+        _tensor(bias, "bias", (N,), dtype, index)
+    _gpu(x_codes, "x_codes")
+    y = x_codes.new_empty((*x_codes.shape[:-1], N), dtype=dtype)
+    T = y.numel() // N
+    if T:
+        n = qmoe.lib.qmoe_mx4_linear_workspace_size(T, N, K)
+        ws = x_codes.new_empty(n)
+        _enqueue(index, qmoe.lib.qmoe_mx4_linear, T, N, K, x_codes.data_ptr(), x_scales.data_ptr(), w_codes.data_ptr(),
+                 w_scales.data_ptr(), _address(bias), y.data_ptr(), code, ws.data_ptr(), n)
     return y
 
 
@@ -126,7 +142,8 @@ class MX4Linear:
 
     def __init__(self, w_codes, w_scales, bias=None):
         _check_mx4(w_codes, w_scales, "w_")
-        _need(w_codes.dim() == 2, "w_codes must be [N, K/2]")
+        if w_codes.dim() != 2:
+            raise ValueError("w_codes must be [N, K/2]")
         self.w_codes, self.w_scales, self.bias = w_codes, w_scales, bias
 
     @classmethod
@@ -161,34 +178,38 @@ class GatedFFN:
             hidden_size=hidden_size, inter_size=inter_size, activation_type=activation_type,
             swiglu_fusion=swiglu_fusion, activation_alpha=activation_alpha, activation_beta=activation_beta,
             swiglu_limit=swiglu_limit, gelu_mode=gelu_mode, act_dtype=qmoe.DTYPE_BF16, reserved=0)
-        if not qmoe.qmoe_gated_ffn_workspace_size(self.cfg, 1, False):
-            raise qmoe.QMoEError(qmoe.QMOE_INVALID_ARGUMENT, qmoe.lib.qmoe_dense_last_error().decode())
+        self._cfg = ctypes.byref(self.cfg)
+        # the forward's refusal of the configuration comes before its other checks
+        status = qmoe.lib.qmoe_gated_ffn_forward(self._cfg, 0, *[None] * 8, 0, None)
+        if status:
+            raise qmoe.QMoEError(status, qmoe.lib.qmoe_dense_last_error().decode())
 
-    def _check_x(self, x, name):
-        _need(x.dim() >= 1 and x.shape[-1] == self.hidden_size, f"{name} must be [..., {self.hidden_size}]")
-        _need(x.dtype == torch.bfloat16, f"{name} must be bfloat16, not {x.dtype}")
-        _need(x.is_contiguous(), f"{name} must be contiguous")
+    def _rows(self, x, name) -> int:
+        if not x.shape or x.shape[-1] != self.hidden_size or x.dtype != torch.bfloat16 or not x.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous bfloat16 tensor [..., {self.hidden_size}], not {x.dtype} "
+                             f"{tuple(x.shape)} with strides {x.stride()}")
+        return x.numel() // self.hidden_size
 
-    def _check_weights(self, w1, w2, b1, b2, dev):
+    def _weights(self, w1, w2, b1, b2, index):
         H, I, bf = self.hidden_size, self.inter_size, torch.bfloat16
-        _tensor(w1, "w1", (2 * I, H), bf, dev)
-        _tensor(w2, "w2", (H, I), bf, dev)
+        _tensor(w1, "w1", (2 * I, H), bf, index)
+        _tensor(w2, "w2", (H, I), bf, index)
         if b1 is not None:
-            _tensor(b1, "b1", (2 * I,), bf, dev)
+            _tensor(b1, "b1", (2 * I,), bf, index)
         if b2 is not None:
-            _tensor(b2, "b2", (H,), bf, dev)
+            _tensor(b2, "b2", (H,), bf, index)
 
     def _forward(self, x, w1, w2, b1, b2, keep):
-        self._check_x(x, "x")
-        dev = x.device
-        self._check_weights(w1, w2, b1, b2, dev)
-        T = x.numel() // self.hidden_size
-        with torch.cuda.device(dev):
-            y = torch.empty_like(x)
-            gu = torch.empty(T, 2 * self.inter_size, dtype=torch.float32, device=dev) if keep else None
-            if T:
-                n = qmoe.qmoe_gated_ffn_workspace_size(self.cfg, T, False)
-                qmoe.qmoe_gated_ffn_forward(self.cfg, T, x, w1, b1, w2, b2, gu, y, _workspace(n, dev), n)
+        T, index = self._rows(x, "x"), x.get_device()
+        self._weights(w1, w2, b1, b2, index)
+        _gpu(x, "x")
+        y = torch.empty_like(x)
+        gu = x.new_empty((T, 2 * self.inter_size), dtype=torch.float32) if keep else None
+        if T:
+            n = qmoe.lib.qmoe_gated_ffn_workspace_size(self._cfg, T, 0)
+            ws = x.new_empty(n, dtype=torch.uint8)
+            _enqueue(index, qmoe.lib.qmoe_gated_ffn_forward, self._cfg, T, x.data_ptr(), w1.data_ptr(), _address(b1),
+                     w2.data_ptr(), _address(b2), _address(gu), y.data_ptr(), ws.data_ptr(), n)
         return y, gu
 
     def forward(self, x, w1, w2, b1=None, b2=None):
@@ -204,18 +225,18 @@ class GatedFFN:
     def backward(self, dy, x, w1, w2, gu, need_dx=True, need_weights=True, bias=False):
         """The gradients of the block for the output's gradient ``dy``; those
         not asked for are None."""
-        self._check_x(dy, "dy")
-        self._check_x(x, "x")
-        _need(dy.shape == x.shape and dy.device == x.device, "dy and x differ in shape or device")
-        dev = x.device
-        self._check_weights(w1, w2, None, None, dev)
-        T, I, H = x.numel() // self.hidden_size, self.inter_size, self.hidden_size
-        _tensor(gu, "gu", (T, 2 * I), torch.float32, dev)
-        with torch.cuda.device(dev):
-            new = lambda want, *s: torch.empty(*s, dtype=torch.bfloat16, device=dev) if want else None  # noqa: E731
-            g = GatedFFNGrads(torch.empty_like(x) if need_dx else None, new(need_weights, 2 * I, H),
-                              new(need_weights, H, I), new(bias, 2 * I), new(bias, H))
-            n = qmoe.qmoe_gated_ffn_workspace_size(self.cfg, T, True)
-            qmoe.qmoe_gated_ffn_backward(self.cfg, T, dy, x, w1, w2, gu, g.dx, g.dw1, g.db1, g.dw2, g.db2,
-                                         _workspace(n, dev), n)
+        T, index, I, H = self._rows(x, "x"), x.get_device(), self.inter_size, self.hidden_size
+        if self._rows(dy, "dy") != T or dy.shape != x.shape or dy.get_device() != index:
+            raise ValueError("dy and x differ in shape or device")
+        self._weights(w1, w2, None, None, index)
+        _tensor(gu, "gu", (T, 2 * I), torch.float32, index)
+        _gpu(x, "x")
+        g = GatedFFNGrads(torch.empty_like(x) if need_dx else None, torch.empty_like(w1) if need_weights else None,
+                          torch.empty_like(w2) if need_weights else None, x.new_empty(2 * I) if bias else None,
+                          x.new_empty(H) if bias else None)
+        n = qmoe.lib.qmoe_gated_ffn_workspace_size(self._cfg, T, 1)
+        ws = x.new_empty(n, dtype=torch.uint8)
+        _enqueue(index, qmoe.lib.qmoe_gated_ffn_backward, self._cfg, T, dy.data_ptr(), x.data_ptr(), w1.data_ptr(),
+                 w2.data_ptr(), gu.data_ptr(), _address(g.dx), _address(g.dw1), _address(g.db1), _address(g.dw2),
+                 _address(g.db2), ws.data_ptr(), n)
         return g
