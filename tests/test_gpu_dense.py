@@ -176,6 +176,37 @@ def test_mx4_linear_writes_only_its_rows(dense):
         assert qmoe.qmoe_dense_read_device_status(ws) == qmoe.QMOE_OK
 
 
+@pytest.mark.parametrize("T", [1, 2, 64, 65, 300])
+def test_dense_calls_stay_inside_their_workspaces(dense, T):
+    """Every call with a workspace of the stated size, between canaries."""
+    from weight_only_quantized_warp_b200 import qmoe
+    H, I = 264, 520
+    p, dy = _block(T, H, I, T)
+    layer = dense.GatedFFN(H, I, swiglu_fusion=1)
+    y, gu = layer.forward_train(p["x"], p["w1"], p["w2"], p["b1"], p["b2"])
+    full = layer.backward(dy, p["x"], p["w1"], p["w2"], gu, bias=True)
+    xq, wq, b = _linear_case(dense, T, 1000, 4096, BF, True, T)
+
+    def guarded(n, call):
+        buf = torch.full((n + 512,), 0xA5, dtype=torch.uint8, device="cuda")
+        call(buf[256:256 + n], n)
+        torch.cuda.synchronize()
+        assert (buf[:256] == 0xA5).all() and (buf[256 + n:] == 0xA5).all()
+
+    out, y2 = torch.empty(T, 1000, dtype=BF, device="cuda"), torch.empty_like(y)
+    guarded(qmoe.qmoe_mx4_linear_workspace_size(T, 1000, 4096), lambda ws, n: qmoe.qmoe_mx4_linear(
+        T, 1000, 4096, *xq, *wq, b, out, qmoe.DTYPE_BF16, ws, n))
+    assert torch.equal(out, dense.mx4_linear(*xq, *wq, b))
+    guarded(qmoe.qmoe_gated_ffn_workspace_size(layer.cfg, T, False), lambda ws, n: qmoe.qmoe_gated_ffn_forward(
+        layer.cfg, T, p["x"], p["w1"], p["b1"], p["w2"], p["b2"], None, y2, ws, n))
+    assert torch.equal(y, y2)
+    g = [torch.empty_like(t) for t in full]
+    guarded(qmoe.qmoe_gated_ffn_workspace_size(layer.cfg, T, True), lambda ws, n: qmoe.qmoe_gated_ffn_backward(
+        layer.cfg, T, dy, p["x"], p["w1"], p["w2"], gu, g[0], g[1], g[3], g[2], g[4], ws, n))
+    for a, b in zip(g, full):
+        assert torch.equal(a, b)
+
+
 def test_mx4_linear_layer(dense):
     n = _gen(11)
     w, b, x = n(200, 352) / 18, n(200).to(BF), n(2, 9, 352).to(BF)

@@ -7,73 +7,61 @@
 
 namespace qmoe {
 
-// Gated activation of one (gate, up) pair. act: QMOE_ACT_* or kActGeluTanh;
-// limit is +inf where nothing is clamped.
+// Gated activation of one (gate, up) pair, h = act(g') (u' + beta) with
+// g' = min(g, limit) and u' = clamp(u, -limit, limit) (limit is +inf and beta 0
+// except for SwiGLU). act(g) = g s(g), where s is
+//   kGateSigmoid   1 / (1 + exp(-z)), z = g (c1 + c3 g^2): SiLU and SwiGLU with
+//                  c3 = 0, and tanh-form GELU, since (1 + tanh v) / 2 is the
+//                  sigmoid of 2 v
+//   kGateErf       the normal distribution function
+//   kGateStep      1 for g > 0, else 0 (ReLU)
+//   kGateOne       1
+// so that one short piece of code, unrolled over a thread's elements, serves
+// every activation (six inlined bodies overflowed the instruction cache: the
+// gradient epilogue then took 60 us for one tile's rows, all of it fetching).
+enum : int { kGateSigmoid = 0, kGateErf = 1, kGateStep = 2, kGateOne = 3 };
 struct GateParams {
-    int act;
-    float alpha, beta, limit;
+    int mode;
+    float c1, c3, beta, limit;
 };
 
-// A clamp that lets NaN through (both comparisons fail).
+// Clamps that let NaN through (both comparisons fail).
 __device__ __forceinline__ float clamp_hi(float v, float hi) { return v > hi ? hi : v; }
 __device__ __forceinline__ float clamp_lo(float v, float lo) { return v < lo ? lo : v; }
 
-// Value and slope of the activation at g (slope skipped when not asked for).
-// Fast exponentials and division: about 2^-21 relative, far inside the bf16
-// rounding that every result goes through.
+// act(g), and its slope when asked for: s + g s'(g). Fast exponentials and
+// division: about 2^-21 relative, far inside the bf16 rounding that every
+// result goes through.
 template <bool SLOPE>
 __device__ __forceinline__ float gate_act(const GateParams& p, float g, float& slope) {
-    switch (p.act) {
-        case QMOE_ACT_RELU:
-            if (SLOPE) slope = g > 0.0f ? 1.0f : (g <= 0.0f ? 0.0f : g);
-            return g < 0.0f ? 0.0f : g;
-        case QMOE_ACT_GELU: {
-            const float cdf = 0.5f * (1.0f + erff(g * 0.70710678118654752f));
-            if (SLOPE) slope = cdf + g * 0.39894228040143268f * __expf(-0.5f * g * g);
-            return g * cdf;
-        }
-        case kActGeluTanh: {
-            const float c = 0.79788456080286536f, t = tanhf(c * (g + 0.044715f * g * g * g));
-            if (SLOPE) slope = 0.5f * (1.0f + t) + 0.5f * g * (1.0f - t * t) * c * (1.0f + 0.134145f * g * g);
-            return 0.5f * g * (1.0f + t);
-        }
-        case QMOE_ACT_SILU:
-        case QMOE_ACT_SWIGLU: {
-            const float a = p.act == QMOE_ACT_SILU ? 1.0f : p.alpha;
-            const float s = __fdividef(1.0f, 1.0f + __expf(-a * g));
-            if (SLOPE) slope = s + a * g * s * (1.0f - s);
-            return g * s;
-        }
-        default:
-            if (SLOPE) slope = 1.0f;
-            return g;
+    if (p.mode == kGateSigmoid) {
+        const float g2 = g * g, s = __fdividef(1.0f, 1.0f + __expf(-g * fmaf(p.c3, g2, p.c1)));
+        if (SLOPE) slope = fmaf(g * fmaf(3.0f * p.c3, g2, p.c1), s * (1.0f - s), s);
+        return g * s;
     }
+    if (p.mode == kGateErf) {
+        const float s = 0.5f * (1.0f + erff(g * 0.70710678118654752f));
+        if (SLOPE) slope = fmaf(g * 0.39894228040143268f, __expf(-0.5f * g * g), s);
+        return g * s;
+    }
+    const bool on = p.mode == kGateOne || g > 0.0f;
+    if (SLOPE) slope = on ? 1.0f : (g <= 0.0f ? 0.0f : g);
+    return on || !(g <= 0.0f) ? g : 0.0f;
 }
 
-// h = act(g') (u' + beta), with SwiGLU's clamps g' and u'.
 __device__ __forceinline__ float gate_value(const GateParams& p, float g, float u) {
     float none;
-    if (p.act == QMOE_ACT_SWIGLU) {
-        g = clamp_hi(g, p.limit);
-        u = clamp_lo(clamp_hi(u, p.limit), -p.limit) + p.beta;
-    }
-    return gate_act<false>(p, g, none) * u;
+    return gate_act<false>(p, clamp_hi(g, p.limit), none) * (clamp_lo(clamp_hi(u, p.limit), -p.limit) + p.beta);
 }
 
-// h and its derivatives by the unclamped g and u.
+// h and its derivatives by g and u (0 beyond a clamp).
 __device__ __forceinline__ float gate_slopes(const GateParams& p, float g, float u, float& hg, float& hu) {
-    float gin = 1.0f, uin = 1.0f;
-    if (p.act == QMOE_ACT_SWIGLU) {
-        gin = g > p.limit ? 0.0f : 1.0f;
-        uin = u > p.limit || u < -p.limit ? 0.0f : 1.0f;
-        g = clamp_hi(g, p.limit);
-        u = clamp_lo(clamp_hi(u, p.limit), -p.limit) + p.beta;
-    }
     float slope;
-    const float a = gate_act<true>(p, g, slope);
-    hg = gin * slope * u;
-    hu = uin * a;
-    return a * u;
+    const float a = gate_act<true>(p, clamp_hi(g, p.limit), slope);
+    const float f = clamp_lo(clamp_hi(u, p.limit), -p.limit) + p.beta;
+    hg = g > p.limit ? 0.0f : slope * f;
+    hu = fabsf(u) > p.limit ? 0.0f : a;
+    return a * f;
 }
 
 // ----------------------------------------------------------------- launchers
@@ -116,11 +104,11 @@ struct DenseArgs {
 size_t dense_pair_workspace(int64_t M, int64_t N, int64_t K);  // re-laid MX4 scales
 cudaError_t launch_dense_pair(const DenseArgs& a, cudaStream_t st);
 
-// The same for few rows of A (kEpiStore and kEpiGate, both operands along k):
-// M up to kStreamRows. `after` says that the kernel before it on the stream,
-// which wrote A, may still be running (it triggers programmatic launch).
+// The same for few rows of A (along k): M up to kStreamRows. early_w: B was not
+// written by the kernel before this one on the stream, so loads of it need not
+// wait for that kernel.
 constexpr int64_t kStreamRows = 64;
-cudaError_t launch_dense_stream(const DenseArgs& a, bool after, cudaStream_t st);
+cudaError_t launch_dense_stream(const DenseArgs& a, bool early_w, cudaStream_t st);
 
 // out[n] = sum_m x[m, n] (x [M, N] bf16) in a fixed order; part: workspace of
 // colsum_bytes(M, N).

@@ -97,11 +97,17 @@ qmoe_status check_ffn(const qmoe_gated_ffn_config* c, int64_t T, GateParams* g) 
     if (T > kMaxDim || c->hidden_size > kMaxDim / 2 || c->inter_size > kMaxDim / 2)
         return bad(QMOE_UNSUPPORTED, "T, hidden_size or inter_size too large");
     if (g) {
-        g->act = c->activation_type == QMOE_ACT_GELU && c->gelu_mode == QMOE_GELU_TANH ? kActGeluTanh
-                                                                                      : c->activation_type;
-        g->alpha = c->activation_alpha == 0.0f ? 1.0f : c->activation_alpha;
-        g->beta = c->activation_beta;
-        g->limit = c->swiglu_limit > 0.0f && std::isfinite(c->swiglu_limit) ? c->swiglu_limit : INFINITY;
+        const int t = c->activation_type;
+        const bool swiglu = t == QMOE_ACT_SWIGLU, tanh = t == QMOE_ACT_GELU && c->gelu_mode == QMOE_GELU_TANH;
+        g->mode = t == QMOE_ACT_RELU       ? kGateStep
+                  : t == QMOE_ACT_IDENTITY ? kGateOne
+                  : t == QMOE_ACT_GELU && !tanh ? kGateErf
+                                                : kGateSigmoid;
+        const float k = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+        g->c1 = tanh ? k : swiglu && c->activation_alpha != 0.0f ? c->activation_alpha : 1.0f;
+        g->c3 = tanh ? k * 0.044715f : 0.0f;
+        g->beta = swiglu ? c->activation_beta : 0.0f;
+        g->limit = swiglu && c->swiglu_limit > 0.0f && std::isfinite(c->swiglu_limit) ? c->swiglu_limit : INFINITY;
     }
     return QMOE_OK;
 }
@@ -118,9 +124,10 @@ struct FfnLayout : Layout {
     }
 };
 
-// Few rows stream the weights, more run on CTA pairs.
-cudaError_t launch_rows(const DenseArgs& a, bool after, cudaStream_t st) {
-    return a.M <= kStreamRows ? launch_dense_stream(a, after, st) : launch_dense_pair(a, st);
+// Few rows stream the weights, more (and the weight gradients, whose rows are
+// weights) run on CTA pairs.
+cudaError_t launch_rows(const DenseArgs& a, bool early_w, cudaStream_t st) {
+    return a.M <= kStreamRows && (a.mx4 || a.a.k_step == 1) ? launch_dense_stream(a, early_w, st) : launch_dense_pair(a, st);
 }
 
 DenseOperand rows_of(const void* p, int64_t ld) { return {p, nullptr, ld, 1}; }   // k along the row
@@ -199,7 +206,7 @@ qmoe_status qmoe_mx4_linear(int64_t T, int64_t N, int64_t K, const uint8_t* x_co
     a.out = y;
     a.status = (int32_t*)workspace;
     a.reset_status = 1;
-    a.scratch = (char*)workspace + Layout().total;
+    a.scratch = T > kStreamRows ? (char*)workspace + Layout().total : nullptr;
     const cudaError_t e = launch_rows(a, false, (cudaStream_t)stream);
     return e == cudaSuccess ? QMOE_OK : cuda_bad(e, "mx4_linear");
 }
@@ -285,7 +292,7 @@ qmoe_status qmoe_gated_ffn_backward(const qmoe_gated_ffn_config* cfg, int64_t T,
     char* ws = (char*)workspace;
     void *h = ws + l.h, *dgu = ws + l.dgu;
     float* part = (float*)(ws + l.part);
-    cudaError_t e = cudaMemsetAsync(workspace, 0, 4, st);
+    cudaError_t e = cudaSuccess;
     auto product = [&](DenseOperand oa, DenseOperand ob, int64_t M, int64_t N, int64_t K, void* out) {
         if (e != cudaSuccess || !out) return;
         DenseArgs a{};
@@ -297,9 +304,9 @@ qmoe_status qmoe_gated_ffn_backward(const qmoe_gated_ffn_config* cfg, int64_t T,
         a.epi = kEpiStore;
         a.out = out;
         a.status = (int32_t*)workspace;
-        e = launch_dense_pair(a, st);
+        e = launch_rows(a, true, st);
     };
-    if (e == cudaSuccess && (dx || dw1 || db1 || dw2)) {
+    if (dx || dw1 || db1 || dw2) {
         DenseArgs a{};
         a.a = rows_of(dy, H);
         a.b = cols_of(w2, I);
@@ -313,7 +320,10 @@ qmoe_status qmoe_gated_ffn_backward(const qmoe_gated_ffn_config* cfg, int64_t T,
         a.gate = gate;
         a.interleaved = cfg->swiglu_fusion == 1;
         a.status = (int32_t*)workspace;
-        e = launch_dense_pair(a, st);
+        a.reset_status = 1;
+        e = launch_rows(a, false, st);
+    } else if (e == cudaSuccess) {
+        e = cudaMemsetAsync(workspace, 0, 4, st);
     }
     product(cols_of(dy, H), cols_of(h, I), H, I, T, dw2);
     product(rows_of(dgu, 2 * I), cols_of(w1, H), T, H, 2 * I, dx);

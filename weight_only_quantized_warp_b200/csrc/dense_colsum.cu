@@ -10,10 +10,12 @@ namespace {
 
 constexpr int kColWarps = 8;
 
-__global__ void __launch_bounds__(kColWarps * 32) colsum_part_kernel(const __nv_bfloat16* __restrict__ x, int64_t M,
+__global__ void __launch_bounds__(kColWarps * 32) colsum_part_kernel(const __nv_bfloat16* x, int64_t M,
                                                                     int64_t N, int64_t rows_per,
-                                                                    float* __restrict__ part) {
+                                                                    float* part) {
     __shared__ float sum[kColWarps][256];
+    pdl_wait();
+    pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t c = int64_t(blockIdx.x) * 256 + lane * 8;  // N is a multiple of 8
     const int64_t m0 = blockIdx.y * rows_per, m1 = min(M, m0 + rows_per);
@@ -42,8 +44,10 @@ __global__ void __launch_bounds__(kColWarps * 32) colsum_part_kernel(const __nv_
     }
 }
 
-__global__ void __launch_bounds__(256) colsum_join_kernel(const float* __restrict__ part, int64_t N, int splits,
-                                                          __nv_bfloat16* __restrict__ out) {
+__global__ void __launch_bounds__(256) colsum_join_kernel(const float* part, int64_t N, int splits,
+                                                          __nv_bfloat16* out) {
+    pdl_wait();
+    pdl_trigger();
     const int64_t n = int64_t(blockIdx.x) * 256 + threadIdx.x;
     if (n >= N) return;
     float s = 0.0f;
@@ -64,9 +68,11 @@ size_t colsum_bytes(int64_t M, int64_t N) { return size_t(col_splits(M, N)) * si
 cudaError_t launch_colsum(const void* x, int64_t M, int64_t N, void* out, float* part, cudaStream_t st) {
     const int64_t s = col_splits(M, N), per = (M + s - 1) / s;
     const unsigned nb = unsigned((N + 255) / 256);
-    colsum_part_kernel<<<dim3(nb, unsigned(s)), kColWarps * 32, 0, st>>>((const __nv_bfloat16*)x, M, N, per, part);
-    colsum_join_kernel<<<nb, 256, 0, st>>>(part, N, int(s), (__nv_bfloat16*)out);
-    return cudaGetLastError();
+    cudaError_t e = launch_kernel(colsum_part_kernel, dim3(nb, unsigned(s)), dim3(kColWarps * 32), 0, st, true,
+                                  (const __nv_bfloat16*)x, M, N, per, part);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(colsum_join_kernel, dim3(nb), dim3(256), 0, st, true, (const float*)part, N, int(s),
+                         (__nv_bfloat16*)out);
 }
 
 }  // namespace qmoe

@@ -39,7 +39,8 @@ constexpr int kABytes = 128 * 128;  // one CTA's A rows of a stage
 
 struct PairArgs {
     int64_t M, N, K;       // N: result columns (h columns for the gate)
-    int tiles_m, tiles_n, nks, z_b, chunks;
+    int tiles_m, tiles_n, nks, chunks;
+    int bn;                // columns of a tile (accumulators, both halves)
     int epi, out_f32, interleaved, vec_out;
     const void* bias;
     void* out;
@@ -56,8 +57,9 @@ struct PairCfg {
     static constexpr int kB = BN / 2 * 128;
     static constexpr int kSA = MX4 ? 1024 : 0, kSB = MX4 ? 2048 : 0;
     static constexpr int kStage = kABytes + kB + kSA + kSB;
-    static constexpr int kStages = 6;
-    static constexpr int kBarOff = kStages * kStage;
+    static constexpr int kStages = MX4 ? 5 : 6;
+    static constexpr int kTurnOff = kStages * kStage;         // 4 KB per epilogue warp
+    static constexpr int kBarOff = kTurnOff + kPEpiWarps * 4096;
     static constexpr int kSmem = kBarOff + 1024 + 1024;
     static_assert(kStage % 1024 == 0 && kSmem <= 227 * 1024, "stages");
 };
@@ -69,30 +71,82 @@ __device__ __forceinline__ void pair_tile(const PairArgs& a, int t, int& tm, int
     tn = r / gm;
 }
 
-// 32 results of one row, columns c0 .. c0 + 31 of an [*, N] bf16 array.
-__device__ __forceinline__ void store32_bf16(__nv_bfloat16* row, int64_t c0, int64_t N, bool vec, const float (&v)[32]) {
-    if (vec && c0 + 32 <= N) {
+// 32 accumulator columns of the warp's lanes, of which `left` belong to the
+// tile (16 at least: the rest is not read).
+__device__ __forceinline__ void tmem_f32(uint32_t t, int left, float (&v)[32]) {
+    if (left >= 32) {
+        uint32_t r[32];
+        tmem_ld32(t, r);
+        tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<uint4*>(row + c0 + 8 * i) =
-                make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
-                           pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
+        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
     } else {
+        float w[16];
+        tmem_ld16(t, w);
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (c0 + i < N) row[c0 + i] = __float2bfloat16_rn(v[i]);
+        for (int i = 0; i < 32; ++i) v[i] = i < 16 ? w[i & 15] : 0.0f;
     }
 }
 
-__device__ __forceinline__ void store32_f32(float* row, int64_t c0, int64_t N, bool vec, const float (&v)[32]) {
-    if (vec && c0 + 32 <= N) {
+// Turn of a 32 x 32 block through a warp's 4 KB: in tensor memory a lane holds
+// a row, in global memory a row wants neighbouring lanes. Lane r writes its
+// row as 16 pairs, pair j at place j ^ (r & 15) of its line (no bank
+// conflicts either way); then half warps read one row each, lane p of a half
+// its pair p.
+__device__ __forceinline__ void turn_put(float2* buf, int lane, const float (&v)[32]) {
+    __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<float4*>(row + c0 + 4 * i) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    for (int j = 0; j < 16; ++j) buf[lane * 16 + (j ^ (lane & 15))] = make_float2(v[2 * j], v[2 * j + 1]);
+    __syncwarp();
+}
+__device__ __forceinline__ float2 turn_get(const float2* buf, int row, int p) { return buf[row * 16 + (p ^ (row & 15))]; }
+
+__device__ __forceinline__ void store_pair(__nv_bfloat16* p, float2 v, bool two, bool vec) {
+    if (two && vec) {
+        *reinterpret_cast<uint32_t*>(p) = pack_bf16(v.x, v.y);
     } else {
+        p[0] = __float2bfloat16_rn(v.x);
+        if (two) p[1] = __float2bfloat16_rn(v.y);
+    }
+}
+__device__ __forceinline__ void store_pair(float* p, float2 v, bool two, bool vec) {
+    if (two && vec) {
+        *reinterpret_cast<float2*>(p) = v;
+    } else {
+        p[0] = v.x;
+        if (two) p[1] = v.y;
+    }
+}
+
+// Loads that stay where they are written, ahead of the arithmetic: a batch of
+// them covers one latency.
+__device__ __forceinline__ void ld_early(const float* p, float& a, float& b, float& c, float& d) {
+    asm volatile("ld.global.cs.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(a), "=f"(b), "=f"(c), "=f"(d) : "l"(p));
+}
+__device__ __forceinline__ void ld_early(const float* p, const float* q, float2& a, float2& b) {
+    asm volatile("ld.global.cs.v2.f32 {%0, %1}, [%2];" : "=f"(a.x), "=f"(a.y) : "l"(p));
+    asm volatile("ld.global.cs.v2.f32 {%0, %1}, [%2];" : "=f"(b.x), "=f"(b.y) : "l"(q));
+}
+
+// A turned block to rows of `ld` elements: `rows` of its 32 rows, `cols` of its
+// 32 columns; out is at its first row and column. vec: pairs are aligned.
+template <typename T>
+__device__ __forceinline__ void turn_store(const float2* buf, T* out, int64_t ld, int rows, int cols, bool vec, int lane) {
+    const int p = lane & 15, hr = lane >> 4;
+    if (2 * p < cols) {
+        const bool two = 2 * p + 1 < cols;
+        T* o = out + hr * ld + 2 * p;
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (c0 + i < N) row[c0 + i] = v[i];
+        for (int i0 = 0; i0 < 16; i0 += 8) {
+            float2 v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = turn_get(buf, 2 * (i0 + i) + hr, p);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (2 * (i0 + i) + hr < rows) store_pair(o, v[i], two, vec);
+                o += 2 * ld;
+            }
+        }
     }
 }
 
@@ -102,7 +156,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
                       const __grid_constant__ CUtensorMap samap, const __grid_constant__ CUtensorMap sbmap,
                       const PairArgs a) {
     using C = PairCfg<MX4>;
-    constexpr int ST = C::kStages, BN = C::BN;
+    constexpr int ST = C::kStages;
+    const int BN = MX4 ? C::BN : a.bn;  // 240 is fixed by the scales' columns
     extern __shared__ uint8_t smem_raw[];
     // the dynamic segment starts at the same address in both CTAs, so the
     // aligned offsets agree
@@ -126,7 +181,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
             mbar_init(smem_u32(&acce[b]), 2 * kPEpiWarps);
         }
         *abort_flag = 0;
-        if (a.reset_status && blockIdx.x == 0) *a.status = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
@@ -138,6 +192,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
     cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    pdl_wait();  // everything up to here touched no global memory
+    pdl_trigger();
+    if (a.reset_status && blockIdx.x == 0 && tid == 0) *a.status = 0;
     const int total = a.tiles_m * a.tiles_n, step = gridDim.x / 2;
 
     if (warp == 0) {
@@ -146,17 +203,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
         int st = 0;
         uint32_t ph = 0;
         bool ok = true;
+        // bytes of both CTAs' copies of a stage
+        const uint32_t bytes = 2u * uint32_t(kABytes + (BMN ? (BN > 128 ? 16384 : 8192) : BN * 64) + C::kSA + C::kSB);
         for (int t = blockIdx.x / 2; ok && t < total; t += step) {
             int tm, tn;
             pair_tile(a, t, tm, tn);
             const int m0 = tm * 256 + int(rank) * 128;
-            const int n0 = EPI == kEpiGate ? tn * 128 : tn * BN + int(rank) * (BN / 2);
+            const int n0 = EPI == kEpiGate ? tn * (BN / 2) : tn * BN + int(rank) * (BN / 2);
             const int zb = EPI == kEpiGate ? int(rank) : 0;
             for (int ks = 0; ks < a.nks; ++ks) {
                 if (!warp_wait(smem_u32(&empty[st]), ph ^ 1u, abort_flag, a.status, kTimeoutNs)) { ok = false; break; }
                 const uint32_t sa = smem_u32(smem + st * C::kStage), sb = sa + kABytes;
                 const uint32_t fb = map_rank(smem_u32(&full[st]), 0);
-                if (rank == 0) mbar_expect_tx_e(smem_u32(&full[st]), 2 * C::kStage, e);
+                if (rank == 0) mbar_expect_tx_e(smem_u32(&full[st]), bytes, e);
                 if (AMN) {
                     tma_3d_pair_e(sa, &amap, m0, ks * 64, 0, fb, e);
                     tma_3d_pair_e(sa + 8192, &amap, m0 + 64, ks * 64, 0, fb, e);
@@ -165,7 +224,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
                 }
                 if (BMN) {
                     tma_3d_pair_e(sb, &bmap, n0, ks * 64, 0, fb, e);
-                    tma_3d_pair_e(sb + 8192, &bmap, n0 + 64, ks * 64, 0, fb, e);
+                    if (BN > 128) tma_3d_pair_e(sb + 8192, &bmap, n0 + 64, ks * 64, 0, fb, e);
                 } else {
                     tma_3d_pair_e(sb, &bmap, ks * (MX4 ? 128 : 64), n0, zb, fb, e);
                 }
@@ -182,11 +241,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
         int st = 0, acc = 0;
         uint32_t ph = 0, cph = 0;
         bool ok = true;
-        const uint32_t tscale = tmem + 2 * BN;  // MX4: A chunk 0, 1 (4 columns each), B chunk 0, 1 (8 each)
+        const uint32_t idesc = idesc_f16(256, BN, AMN, BMN);
+        const uint32_t tscale = tmem + 2 * C::BN;  // MX4: A chunk 0, 1 (4 columns each), B chunk 0, 1 (8 each)
         for (int t = blockIdx.x / 2; ok && t < total; t += step) {
             if (!warp_wait_cluster(smem_u32(&acce[acc]), cph ^ 1u, abort_flag, a.status)) break;
             tc_fence_after();
-            const uint32_t d = tmem + uint32_t(acc * BN);
+            const uint32_t d = tmem + uint32_t(acc * C::BN);
             for (int ks = 0; ks < a.nks; ++ks) {
                 if (!warp_wait_cluster(smem_u32(&full[st]), ph, abort_flag, a.status)) { ok = false; break; }
                 tc_fence_after();
@@ -203,7 +263,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
                     const uint64_t ad = desc_sw128(sa), bd = desc_sw128(sb);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        mma_mx4_pair_e(d, ad + uint64_t(2 * kk), bd + uint64_t(2 * kk), idesc_mx4(256, BN, 2 * (kk & 1)),
+                        mma_mx4_pair_e(d, ad + uint64_t(2 * kk), bd + uint64_t(2 * kk), idesc_mx4(256, C::BN, 2 * (kk & 1)),
                                        tscale + 4 * (kk >> 1), tscale + 8 + 8 * (kk >> 1), kk > 0 ? 1u : acc0, e);
                 } else {
                     const uint64_t ad = AMN ? desc_mn128(sa) : desc_sw128(sa);
@@ -211,7 +271,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)  // 16 k: 32 bytes into each line, or 16 lines on
                         mma_bf16_pair_e(d, ad + uint64_t((AMN ? 128 : 2) * kk), bd + uint64_t((BMN ? 128 : 2) * kk),
-                                        idesc_f16(256, BN, AMN, BMN), kk > 0 ? 1u : acc0, e);
+                                        idesc, kk > 0 ? 1u : acc0, e);
                 }
                 mma_commit_pair_e(smem_u32(&empty[st]), e);
                 if (++st == ST) { st = 0; ph ^= 1u; }
@@ -223,6 +283,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
     } else if (warp >= kPEpi0) {
         // ------------------------------------------------------- epilogue
         const int qd = warp & 3, half = (warp - kPEpi0) >> 2;
+        float2* turn = reinterpret_cast<float2*>(smem + C::kTurnOff + (warp - kPEpi0) * 4096);
         int acc = 0;
         uint32_t cph = 0;
         for (int t = blockIdx.x / 2; t < total; t += step) {
@@ -230,131 +291,118 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
             pair_tile(a, t, tm, tn);
             if (!warp_wait(smem_u32(&accf[acc]), cph, abort_flag, a.status, kTimeoutNs)) break;
             tc_fence_after();
-            const uint32_t tb = tmem + (uint32_t(qd * 32) << 16) + uint32_t(acc * BN);
-            const int64_t m = int64_t(tm) * 256 + rank * 128 + qd * 32 + lane;
-            const bool row = m < a.M;
+            const uint32_t tb = tmem + (uint32_t(qd * 32) << 16) + uint32_t(acc * C::BN);
+            const int64_t m0 = int64_t(tm) * 256 + rank * 128 + qd * 32;
+            const int rows = int(max(int64_t(0), min(int64_t(32), a.M - m0)));
             if (EPI == kEpiStore) {
+                const int64_t end = min(a.N, int64_t(tn + 1) * BN);
                 for (int c = half * 32; c < BN; c += 64) {
                     const int64_t n = int64_t(tn) * BN + c;
-                    if (n >= a.N) break;  // uniform over the warp
+                    if (n >= end) break;  // uniform over the warp
+                    const int cols = int(min(int64_t(32), end - n));
                     float v[32];
-                    if (BN - c >= 32) {
-                        uint32_t r[32];
-                        tmem_ld32(tb + uint32_t(c), r);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-                    } else {
-                        float w[16];
-                        tmem_ld16(tb + uint32_t(c), w);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = i < 16 ? w[i & 15] : 0.0f;
-                    }
-                    // the tile's last columns end inside a chunk when BN is not a multiple of 32
-                    const int64_t end = min(a.N, int64_t(tn + 1) * BN);
+                    tmem_f32(tb + uint32_t(c), BN - c, v);
                     if (a.bias) {
+                        const float b = lane >= cols ? 0.0f
+                                        : a.out_f32  ? ((const float*)a.bias)[n + lane]
+                                                     : __bfloat162float(((const __nv_bfloat16*)a.bias)[n + lane]);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (n + i < end)
-                                v[i] += a.out_f32 ? __ldg((const float*)a.bias + n + i)
-                                                  : __bfloat162float(((const __nv_bfloat16*)a.bias)[n + i]);
+                        for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xffffffffu, b, i);
                     }
-                    if (row) {
-                        if (a.out_f32) store32_f32((float*)a.out + m * a.N, n, end, a.vec_out, v);
-                        else store32_bf16((__nv_bfloat16*)a.out + m * a.N, n, end, a.vec_out, v);
-                    }
+                    turn_put(turn, lane, v);
+                    if (a.out_f32) turn_store(turn, (float*)a.out + m0 * a.N + n, a.N, rows, cols, a.vec_out, lane);
+                    else turn_store(turn, (__nv_bfloat16*)a.out + m0 * a.N + n, a.N, rows, cols, a.vec_out, lane);
                 }
             } else if (EPI == kEpiGate) {
-                for (int c = half * 32; c < 128; c += 64) {
-                    const int64_t n = int64_t(tn) * 128 + c;
+                const int bh = BN / 2;
+                for (int c = half * 32; c < bh; c += 64) {
+                    const int64_t n = int64_t(tn) * bh + c;
                     if (n >= a.N) break;
-                    uint32_t rg[32], ru[32];
-                    tmem_ld32(tb + uint32_t(c), rg);
-                    tmem_ld32(tb + uint32_t(128 + c), ru);
-                    tmem_wait_ld();
-                    float g[32], u[32], h[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        g[i] = __uint_as_float(rg[i]);
-                        u[i] = __uint_as_float(ru[i]);
-                    }
+                    const int cols = int(min(int64_t(min(32, bh - c)), a.N - n));  // a multiple of 8, as N and bh are
+                    float g[32], u[32];
+                    tmem_f32(tb + uint32_t(c), bh - c, g);
+                    tmem_f32(tb + uint32_t(bh + c), bh - c, u);
                     if (a.bias) {
                         const __nv_bfloat16* b = (const __nv_bfloat16*)a.bias;
+                        float bg = 0.0f, bu = 0.0f;
+                        if (lane < cols) {
+                            bg = __bfloat162float(b[a.interleaved ? 2 * (n + lane) : n + lane]);
+                            bu = __bfloat162float(b[a.interleaved ? 2 * (n + lane) + 1 : a.N + n + lane]);
+                        }
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (n + i < a.N) {
-                                g[i] += __bfloat162float(b[a.interleaved ? 2 * (n + i) : n + i]);
-                                u[i] += __bfloat162float(b[a.interleaved ? 2 * (n + i) + 1 : a.N + n + i]);
-                            }
+                        for (int i = 0; i < 32; ++i) {
+                            g[i] += __shfl_sync(0xffffffffu, bg, i);
+                            u[i] += __shfl_sync(0xffffffffu, bu, i);
+                        }
                     }
-                    if (row && a.gu) {
-                        float* gr = a.gu + m * 2 * a.N;
-                        if (a.interleaved) {  // N is a multiple of 8: whole groups of four pairs
+                    if (a.gu) {
+                        float* gr = a.gu + m0 * 2 * a.N;
+                        if (a.interleaved) {
 #pragma unroll
-                            for (int i = 0; i < 32; i += 2)
-                                if (n + i < a.N)
-                                    *reinterpret_cast<float4*>(gr + 2 * (n + i)) = make_float4(g[i], u[i], g[i + 1], u[i + 1]);
+                            for (int k = 0; k < 32; k += 16) {
+                                float w[32];
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) {
+                                    w[2 * i] = g[k + i];
+                                    w[2 * i + 1] = u[k + i];
+                                }
+                                turn_put(turn, lane, w);
+                                turn_store(turn, gr + 2 * (n + k), 2 * a.N, rows, 2 * (cols - k), true, lane);
+                            }
                         } else {
-                            store32_f32(gr, n, a.N, true, g);
-                            store32_f32(gr + a.N, n, a.N, true, u);
+                            turn_put(turn, lane, g);
+                            turn_store(turn, gr + n, 2 * a.N, rows, cols, true, lane);
+                            turn_put(turn, lane, u);
+                            turn_store(turn, gr + a.N + n, 2 * a.N, rows, cols, true, lane);
                         }
                     }
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) h[i] = gate_value(a.gate, g[i], u[i]);
-                    if (row) store32_bf16((__nv_bfloat16*)a.out + m * a.N, n, a.N, true, h);
+                    for (int i = 0; i < 32; ++i) g[i] = gate_value(a.gate, g[i], u[i]);
+                    turn_put(turn, lane, g);
+                    turn_store(turn, (__nv_bfloat16*)a.out + m0 * a.N + n, a.N, rows, cols, true, lane);
                 }
             } else {
+                const int p = lane & 15, hr = lane >> 4;
+                const int64_t end = min(a.N, int64_t(tn + 1) * BN);
                 for (int c = half * 32; c < BN; c += 64) {
                     const int64_t n = int64_t(tn) * BN + c;
-                    if (n >= a.N) break;
-                    uint32_t rd[32];
-                    tmem_ld32(tb + uint32_t(c), rd);
-                    tmem_wait_ld();
-                    const float* gr = a.gu + m * 2 * a.N;
-                    __nv_bfloat16* dr = (__nv_bfloat16*)a.dgu + m * 2 * a.N;
-                    __nv_bfloat16* hr = (__nv_bfloat16*)a.out + m * a.N;
+                    if (n >= end) break;
+                    float v[32];
+                    tmem_f32(tb + uint32_t(c), BN - c, v);
+                    turn_put(turn, lane, v);
+                    const int64_t col = n + 2 * p;
+                    // interleaved: (g, u, g, u) of the pair; else g and u pairs N apart
+                    const float* gr = a.gu + (m0 + hr) * 2 * a.N + (a.interleaved ? 2 * col : col);
+                    __nv_bfloat16* dr = (__nv_bfloat16*)a.dgu + (m0 + hr) * 2 * a.N + (a.interleaved ? 2 * col : col);
+                    __nv_bfloat16* hp = (__nv_bfloat16*)a.out + (m0 + hr) * a.N + col;
+                    const int mine = col < end ? rows - hr : 0;  // N is even: whole pairs
+                    if (mine > 0)
+                    for (int i0 = 0; i0 < 16; i0 += 8) {
+                        float2 g[8], u[8];
 #pragma unroll
-                    for (int i = 0; i < 32; i += 8) {  // N is a multiple of 8
-                        if (!row || n + i >= a.N) break;
-                        float g[8], u[8];
-                        if (a.interleaved) {
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const float4 w = *reinterpret_cast<const float4*>(gr + 2 * (n + i) + 4 * j);
-                                g[2 * j] = w.x; u[2 * j] = w.y; g[2 * j + 1] = w.z; u[2 * j + 1] = w.w;
-                            }
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                const float4 w = *reinterpret_cast<const float4*>(gr + n + i + 4 * j);
-                                const float4 x = *reinterpret_cast<const float4*>(gr + a.N + n + i + 4 * j);
-                                g[4 * j] = w.x; g[4 * j + 1] = w.y; g[4 * j + 2] = w.z; g[4 * j + 3] = w.w;
-                                u[4 * j] = x.x; u[4 * j + 1] = x.y; u[4 * j + 2] = x.z; u[4 * j + 3] = x.w;
-                            }
+                        for (int i = 0; i < 8; ++i) {
+                            // a row past the end reads the last one: no branch keeps a load back
+                            const float* r = gr + int64_t(min(2 * (i0 + i), (mine - 1) & ~1)) * 2 * a.N;
+                            if (a.interleaved) ld_early(r, g[i].x, u[i].x, g[i].y, u[i].y);
+                            else ld_early(r, r + a.N, g[i], u[i]);
                         }
-                        float dg[8], du[8], h[8];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            float hg, hu;
-                            h[j] = gate_slopes(a.gate, g[j], u[j], hg, hu);
-                            const float dh = __uint_as_float(rd[i + j]);
-                            dg[j] = dh * hg;
-                            du[j] = dh * hu;
-                        }
-                        *reinterpret_cast<uint4*>(hr + n + i) = make_uint4(pack_bf16(h[0], h[1]), pack_bf16(h[2], h[3]),
-                                                                           pack_bf16(h[4], h[5]), pack_bf16(h[6], h[7]));
-                        if (a.interleaved) {
-#pragma unroll
-                            for (int j = 0; j < 2; ++j)
-                                *reinterpret_cast<uint4*>(dr + 2 * (n + i) + 8 * j) =
-                                    make_uint4(pack_bf16(dg[4 * j], du[4 * j]), pack_bf16(dg[4 * j + 1], du[4 * j + 1]),
-                                               pack_bf16(dg[4 * j + 2], du[4 * j + 2]), pack_bf16(dg[4 * j + 3], du[4 * j + 3]));
-                        } else {
-                            *reinterpret_cast<uint4*>(dr + n + i) = make_uint4(pack_bf16(dg[0], dg[1]), pack_bf16(dg[2], dg[3]),
-                                                                               pack_bf16(dg[4], dg[5]), pack_bf16(dg[6], dg[7]));
-                            *reinterpret_cast<uint4*>(dr + a.N + n + i) =
-                                make_uint4(pack_bf16(du[0], du[1]), pack_bf16(du[2], du[3]), pack_bf16(du[4], du[5]),
-                                           pack_bf16(du[6], du[7]));
+                        for (int i = 0; i < 8; ++i) {
+                            const int row = 2 * (i0 + i) + hr;
+                            if (row - hr >= mine) break;
+                            const float2 dh = turn_get(turn, row, p);
+                            float gx, ux, gy, uy;
+                            const float hx = gate_slopes(a.gate, g[i].x, u[i].x, gx, ux);
+                            const float hy = gate_slopes(a.gate, g[i].y, u[i].y, gy, uy);
+                            *reinterpret_cast<uint32_t*>(hp + int64_t(i0 + i) * 2 * a.N) = pack_bf16(hx, hy);
+                            __nv_bfloat16* d = dr + int64_t(i0 + i) * 4 * a.N;
+                            if (a.interleaved) {
+                                *reinterpret_cast<uint2*>(d) =
+                                    make_uint2(pack_bf16(dh.x * gx, dh.x * ux), pack_bf16(dh.y * gy, dh.y * uy));
+                            } else {
+                                *reinterpret_cast<uint32_t*>(d) = pack_bf16(dh.x * gx, dh.y * gy);
+                                *reinterpret_cast<uint32_t*>(d + a.N) = pack_bf16(dh.x * ux, dh.y * uy);
+                            }
                         }
                     }
                     __syncwarp();
@@ -387,6 +435,8 @@ __global__ void __launch_bounds__(256) mx4_tile_scales_kernel(const uint8_t* sa,
                                                               uint32_t* oa, const uint8_t* sb, int64_t rows_b,
                                                               int tr_b, int tiles_b, uint32_t* ob, int64_t pitch,
                                                               int chunks) {
+    pdl_wait();
+    pdl_trigger();
     const bool second = blockIdx.y == 1;
     const uint8_t* s = second ? sb : sa;
     const int64_t rows = second ? rows_b : rows_a;
@@ -418,8 +468,29 @@ cudaError_t launch_one(const CUtensorMap (&maps)[4], const PairArgs& a, cudaStre
     if (e != cudaSuccess) return e;
     const int64_t tiles = int64_t(a.tiles_m) * a.tiles_n, pairs = sm_count() / 2;
     const int grid = 2 * int(tiles < pairs ? tiles : pairs);
-    kern<<<grid, kPThreads, PairCfg<MX4>::kSmem, st>>>(maps[0], maps[1], maps[2], maps[3], a);
-    return cudaGetLastError();
+    return launch_kernel(kern, dim3(unsigned(grid)), dim3(kPThreads), PairCfg<MX4>::kSmem, st, true, maps[0], maps[1],
+                         maps[2], maps[3], a);
+}
+
+// Tile columns of a bf16 product: 256 where the tiles fill many rounds of the
+// pairs. With few rounds a narrower tile can save a large part of the last,
+// half-empty one: the width (a multiple of 32, at least 128) with the smallest
+// rounds x (BN + 256), a stage's operand bytes per CTA, which is what a stage
+// takes below 256 columns. Measured at T = 1024, H = I = 2880 (160 columns)
+// against 256 throughout: forward 56.7 against 67.6 us, training step 194
+// against 217 us; 160 columns at T = 4096, H = 4096, I = 14336 (where the rule
+// keeps 256) take 3792 us against 3120.
+int pair_width(int64_t tiles_m, int64_t n, int pairs) {
+    int best = 256;
+    int64_t cost = INT64_MAX;
+    for (int bn = 256; bn >= 128; bn -= 32) {
+        const int64_t tiles = tiles_m * ((n + bn - 1) / bn), c = (tiles + pairs - 1) / pairs * (bn + 256);
+        if (c < cost) {
+            cost = c;
+            best = bn;
+        }
+    }
+    return best;
 }
 
 int64_t pair_chunks(int64_t K) { return 2 * ((K + 255) / 256); }
@@ -433,14 +504,17 @@ size_t dense_pair_workspace(int64_t M, int64_t N, int64_t K) {
 }
 
 cudaError_t launch_dense_pair(const DenseArgs& d, cudaStream_t st) {
-    const int BN = d.mx4 ? 240 : 256;
     const bool gate = d.epi == kEpiGate;
     PairArgs a{};
     a.M = d.M;
     a.N = gate ? d.N / 2 : d.N;
     a.K = d.K;
     a.tiles_m = int((d.M + 255) / 256);
-    a.tiles_n = int((a.N + (gate ? 128 : BN) - 1) / (gate ? 128 : BN));
+    const int BN = d.mx4 ? 240 : pair_width(a.tiles_m, d.N, sm_count() / 2);
+    a.bn = BN;
+    const int64_t tn = (a.N + (gate ? BN / 2 : BN) - 1) / (gate ? BN / 2 : BN);
+    if (int64_t(a.tiles_m) * tn > (int64_t(1) << 30)) return cudaErrorInvalidValue;
+    a.tiles_n = int(tn);
     a.nks = int((d.K + (d.mx4 ? 255 : 63)) / (d.mx4 ? 256 : 64));
     a.epi = d.epi;
     a.out_f32 = d.out_f32;
@@ -452,20 +526,21 @@ cudaError_t launch_dense_pair(const DenseArgs& d, cudaStream_t st) {
     a.gate = d.gate;
     a.status = d.status;
     a.reset_status = d.reset_status;
-    a.vec_out = (d.N * (d.out_f32 ? 4 : 2)) % 16 == 0 && (reinterpret_cast<uintptr_t>(d.out) & 15) == 0;
-    if (int64_t(a.tiles_m) * a.tiles_n > (int64_t(1) << 30)) return cudaErrorInvalidValue;
+    a.vec_out = d.N % 2 == 0 && (reinterpret_cast<uintptr_t>(d.out) & (d.out_f32 ? 7 : 3)) == 0;
     CUtensorMap maps[4] = {};
     cudaError_t e;
     if (d.mx4) {
+        if (!d.scratch) return cudaErrorInvalidValue;
         const int64_t c = pair_chunks(d.K), ta = int64_t(a.tiles_m) * 2, tb = a.tiles_n;
         a.chunks = int(c);
         uint8_t* oa = (uint8_t*)d.scratch;
         uint8_t* ob = oa + up256(ta * c * 512);
         const int64_t words = (ta > 2 * tb ? ta : 2 * tb) * 128 * ((c + 3) / 4);
         const int64_t blocks = (words + 255) / 256;
-        mx4_tile_scales_kernel<<<dim3(unsigned(blocks < 4096 ? blocks : 4096), 2), 256, 0, st>>>(
-            d.a.s, d.M, 128, int(ta), (uint32_t*)oa, d.b.s, d.N, BN, int(tb), (uint32_t*)ob, d.K / 32, int(c));
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        e = launch_kernel(mx4_tile_scales_kernel, dim3(unsigned(blocks < 4096 ? blocks : 4096), 2), dim3(256), 0, st, true,
+                          d.a.s, d.M, 128, int(ta), (uint32_t*)oa, d.b.s, d.N, BN, int(tb), (uint32_t*)ob, d.K / 32,
+                          int(c));
+        if (e != cudaSuccess) return e;
         for (int i = 0; i < 2; ++i) {
             const MapSpec s = i ? mx4_spec(d.b.p, d.N, d.K, uint32_t(BN / 2)) : mx4_spec(d.a.p, d.M, d.K, 128);
             if ((e = encode_map(&maps[i], s)) != cudaSuccess) return e;
@@ -487,9 +562,9 @@ cudaError_t launch_dense_pair(const DenseArgs& d, cudaStream_t st) {
     if (gate) {  // gate and up rows: every other row, or the two halves
         DenseOperand w = d.b;
         if (d.interleaved) w.row *= 2;
-        e = encode_map(&maps[1], bf16_spec(w, a.N, d.K, 128, d.interleaved ? d.b.row : a.N * d.b.row));
+        e = encode_map(&maps[1], bf16_spec(w, a.N, d.K, uint32_t(BN / 2), d.interleaved ? d.b.row : a.N * d.b.row));
     } else {
-        e = encode_map(&maps[1], bf16_spec(d.b, d.N, d.K, 128, 0));
+        e = encode_map(&maps[1], bf16_spec(d.b, d.N, d.K, uint32_t(BN / 2), 0));
     }
     if (e != cudaSuccess) return e;
     const bool amn = d.a.k_step != 1, bmn = d.b.k_step != 1;

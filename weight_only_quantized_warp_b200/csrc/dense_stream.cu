@@ -5,7 +5,9 @@
 // two accumulators) and the tokens its N, padded to NT = 16, 32 or 64, so
 // the tensor core takes both operands as they lie (MX4 codes undecoded) and
 // the CTA does nothing per weight but move it: TMA fills a ring of 128-byte
-// wide stages that an MMA warp empties.
+// wide stages that an MMA warp empties. The backward pass's products (dh = dy w2,
+// dx = dgu w1) run across the rows of W in memory: there a stage is 64 lines of
+// 128 W columns and the descriptor says MN-major.
 //
 // K is split over the CTAs of a cluster so that about two CTAs per SM stream
 // at once; their fp32 partials meet in shared memory and are added in rank
@@ -29,11 +31,12 @@ constexpr int kSW = 128 * 128;  // W rows of a stage, one accumulator
 struct StreamArgs {
     int64_t N, K, I;  // N: rows of W per accumulator (h columns for the gate)
     int T, nks, splits;
-    int out_f32, interleaved, after;
+    int out_f32, interleaved, early_w;
     const uint8_t *ws, *xs;  // MX4 scales
     const void* bias;
     void* out;
-    float* gu;
+    float* gu;             // kEpiGate: written when not null; kEpiGateBwd: read
+    __nv_bfloat16* dgu;    // kEpiGateBwd
     GateParams gate;
     int32_t* status;
     int reset_status;
@@ -54,29 +57,51 @@ struct StreamCfg {
     static_assert(kStages >= 2 && kStage % 1024 == 0 && kSmem <= 113 * 1024, "two CTAs per SM");
 };
 
-// The results of W row n for token t.
-template <bool GATE>
-__device__ __forceinline__ void stream_emit(const StreamArgs& a, int t, int64_t n, float g, float u, float bg, float bu) {
-    if (GATE) {
-        g += bg;
-        u += bu;
-        if (a.gu) {
-            float* r = a.gu + int64_t(t) * 2 * a.N;
-            r[a.interleaved ? 2 * n : n] = g;
-            r[a.interleaved ? 2 * n + 1 : a.N + n] = u;
+// The results of W row n for NB tokens t, t + step, ... (of `left`): acc holds
+// their sums (gate and up for the gate).
+template <int EPI, int NB>
+__device__ __forceinline__ void stream_emit(const StreamArgs& a, int t, int step, int left, int64_t n,
+                                            const float (&g)[NB], const float (&u)[NB], float bg, float bu) {
+    float sg[NB], su[NB];
+    if (EPI == kEpiGateBwd) {  // all loads before any use
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+            const float* r = a.gu + int64_t(t + min(j, left - 1) * step) * 2 * a.N;
+            asm volatile("ld.global.f32 %0, [%1];" : "=f"(sg[j]) : "l"(r + (a.interleaved ? 2 * n : n)));
+            asm volatile("ld.global.f32 %0, [%1];" : "=f"(su[j]) : "l"(r + (a.interleaved ? 2 * n + 1 : a.N + n)));
         }
-        reinterpret_cast<__nv_bfloat16*>(a.out)[t * a.N + n] = __float2bfloat16_rn(gate_value(a.gate, g, u));
-    } else if (a.out_f32) {
-        reinterpret_cast<float*>(a.out)[t * a.N + n] = g + bg;
-    } else {
-        reinterpret_cast<__nv_bfloat16*>(a.out)[t * a.N + n] = __float2bfloat16_rn(g + bg);
+    }
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+        if (j >= left) break;
+        const int64_t tt = t + j * step;
+        __nv_bfloat16* ob = reinterpret_cast<__nv_bfloat16*>(a.out) + tt * a.N + n;
+        const int64_t gi = tt * 2 * a.N + (a.interleaved ? 2 * n : n), ui = a.interleaved ? gi + 1 : gi + a.N;
+        if (EPI == kEpiGate) {
+            const float vg = g[j] + bg, vu = u[j] + bu;
+            if (a.gu) {
+                a.gu[gi] = vg;
+                a.gu[ui] = vu;
+            }
+            *ob = __float2bfloat16_rn(gate_value(a.gate, vg, vu));
+        } else if (EPI == kEpiGateBwd) {
+            float hg, hu;
+            *ob = __float2bfloat16_rn(gate_slopes(a.gate, sg[j], su[j], hg, hu));
+            a.dgu[gi] = __float2bfloat16_rn(g[j] * hg);
+            a.dgu[ui] = __float2bfloat16_rn(g[j] * hu);
+        } else if (a.out_f32) {
+            reinterpret_cast<float*>(a.out)[tt * a.N + n] = g[j] + bg;
+        } else {
+            *ob = __float2bfloat16_rn(g[j] + bg);
+        }
     }
 }
 
-template <bool MX4, bool GATE, int NT>
+template <bool MX4, int EPI, bool WMN, int NT>
 __global__ void __launch_bounds__(kSThreads, 2)
     dense_stream_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                         const StreamArgs a) {
+    constexpr bool GATE = EPI == kEpiGate;
     using C = StreamCfg<MX4, GATE, NT>;
     constexpr int ST = C::kStages, KE = MX4 ? 128 : 64;  // map elements of a stage along k
     extern __shared__ uint8_t smem_raw[];
@@ -98,7 +123,6 @@ __global__ void __launch_bounds__(kSThreads, 2)
         }
         mbar_init(smem_u32(accf), 1);
         *abort_flag = 0;
-        if (a.reset_status && blockIdx.x == 0) *a.status = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
@@ -110,7 +134,13 @@ __global__ void __launch_bounds__(kSThreads, 2)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    pdl_trigger();
+    if (!(warp == 0 && a.early_w)) {  // everything up to here touched no global memory
+        pdl_wait();
+        // not before the wait: the next kernel's early loads count on all that
+        // came before this one being complete
+        pdl_trigger();
+    }
+    if (a.reset_status && blockIdx.x == 0 && tid == 32) *a.status = 0;
 
     if (warp == 0) {
         // ------------------------------------------------------- producer
@@ -121,16 +151,21 @@ __global__ void __launch_bounds__(kSThreads, 2)
         auto load_w = [&](int ks, int s) {
             const uint32_t sw = smem_u32(smem + s * C::kStage), fb = smem_u32(&full[s]);
             mbar_expect_tx_e(fb, C::kStage - C::kS, e);
-            tma_3d_e(sw, &wmap, ks * KE, n0, 0, fb, e);
+            if (WMN) {
+                tma_3d_e(sw, &wmap, n0, ks * 64, 0, fb, e);
+                tma_3d_e(sw + 8192, &wmap, n0 + 64, ks * 64, 0, fb, e);
+            } else {
+                tma_3d_e(sw, &wmap, ks * KE, n0, 0, fb, e);
+            }
             if (GATE) tma_3d_e(sw + kSW, &wmap, ks * KE, n0, 1, fb, e);
         };
         auto load_x = [&](int ks, int s) {
             tma_3d_e(smem_u32(smem + s * C::kStage) + kSW * (GATE ? 2 : 1), &xmap, ks * KE, 0, 0, smem_u32(&full[s]), e);
         };
-        // W does not depend on the kernel before this one: the ring fills
-        // with it first
+        // where W does not depend on the kernel before this one, the ring fills
+        // with it while that kernel drains
         for (int i = 0; i < first; ++i) load_w(ks0 + i, i);
-        if (a.after) pdl_wait();
+        if (a.early_w) pdl_wait();
         for (int i = 0; i < first; ++i) load_x(ks0 + i, i);
         for (int ks = ks0 + first; ks < ks1; ++ks) {
             if (!warp_wait(smem_u32(&empty[st]), ph, abort_flag, a.status, kTimeoutNs)) break;
@@ -149,7 +184,7 @@ __global__ void __launch_bounds__(kSThreads, 2)
             if (!warp_wait(smem_u32(&full[st]), ph, abort_flag, a.status, kTimeoutNs)) { ok = false; break; }
             tc_fence_after();
             const uint32_t sw = smem_u32(smem + st * C::kStage), sx = sw + kSW * (GATE ? 2 : 1);
-            const uint64_t wd = desc_sw128(sw), xd = desc_sw128(sx);
+            const uint64_t wd = WMN ? desc_mn128(sw) : desc_sw128(sw), xd = desc_sw128(sx);
             const uint32_t acc0 = ks > ks0 ? 1u : 0u;
             if constexpr (MX4) {
 #pragma unroll
@@ -159,11 +194,11 @@ __global__ void __launch_bounds__(kSThreads, 2)
                     mma_mx4_e(tmem, wd + uint64_t(2 * kk), xd + uint64_t(2 * kk), idesc_mx4(128, NT, 2 * (kk & 1)),
                               ts + 4 * (kk >> 1), ts + 8 + 4 * (kk >> 1), kk > 0 ? 1u : acc0, e);
             } else {
-                constexpr uint32_t id = idesc_f16(128, NT, false, false);
+                constexpr uint32_t id = idesc_f16(128, NT, WMN, false);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) {
                     const uint32_t acc = kk > 0 ? 1u : acc0;
-                    mma_bf16_ss_e(tmem, wd + uint64_t(2 * kk), xd + uint64_t(2 * kk), id, acc, e);
+                    mma_bf16_ss_e(tmem, wd + uint64_t((WMN ? 128 : 2) * kk), xd + uint64_t(2 * kk), id, acc, e);
                     if (GATE)
                         mma_bf16_ss_e(tmem + NT, desc_sw128(sw + kSW) + uint64_t(2 * kk), xd + uint64_t(2 * kk), id, acc, e);
                 }
@@ -177,7 +212,6 @@ __global__ void __launch_bounds__(kSThreads, 2)
         bool ok = true;
         if constexpr (MX4) {
             // ------------------------------------------- scales: row et of W and X
-            if (a.after) pdl_wait();
             const int64_t pitch = a.K / 32, nw = n0 + et;
             int st = 0;
             uint32_t ph = 0;
@@ -233,9 +267,6 @@ __global__ void __launch_bounds__(kSThreads, 2)
             }
         }
         float* part = reinterpret_cast<float*>(smem);  // [accumulator][token][128]
-        // the output (and, when this is the call's second product, its inputs'
-        // buffer) may still be in use by the kernel before
-        if (a.after) pdl_wait();
         if (ok) {
             for (int t0 = 0; t0 < a.T; t0 += 16) {
                 float v[16], u[16];
@@ -243,14 +274,18 @@ __global__ void __launch_bounds__(kSThreads, 2)
                 if (GATE) tmem_ld16(tb + uint32_t(NT + t0), u);
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
-                    if (t0 + j >= a.T) break;
-                    const float g = some ? v[j] : 0.0f, up = GATE && some ? u[j] : 0.0f;
-                    if (a.splits > 1) {
-                        part[(t0 + j) * 128 + row] = g;
-                        if (GATE) part[(NT + t0 + j) * 128 + row] = up;
-                    } else if (valid) {
-                        stream_emit<GATE>(a, t0 + j, n, g, up, bg, bu);
+                    if (!some) v[j] = 0.0f;
+                    if (!GATE || !some) u[j] = 0.0f;
+                }
+                if (a.splits > 1) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        if (t0 + j >= a.T) break;
+                        part[(t0 + j) * 128 + row] = v[j];
+                        if (GATE) part[(NT + t0 + j) * 128 + row] = u[j];
                     }
+                } else if (valid) {
+                    stream_emit<EPI, 16>(a, t0, 1, a.T - t0, n, v, u, bg, bu);
                 }
                 __syncwarp();
             }
@@ -258,14 +293,21 @@ __global__ void __launch_bounds__(kSThreads, 2)
         if (a.splits > 1) {
             cluster_sync_all();
             if (valid) {
+                constexpr int NB = 4;
                 const uint32_t base = smem_u32(part) + row * 4;
-                for (int t = rank; t < a.T; t += a.splits) {
-                    float g = 0.0f, u = 0.0f;
+                for (int t = rank; t < a.T; t += NB * a.splits) {
+                    const int left = (a.T - t + a.splits - 1) / a.splits;
+                    float g[NB] = {}, u[NB] = {};
                     for (int s = 0; s < a.splits; ++s) {
-                        g += ld_cluster_f32(map_rank(base + t * 512, s));
-                        if (GATE) u += ld_cluster_f32(map_rank(base + (NT + t) * 512, s));
+                        const uint32_t from = map_rank(base, uint32_t(s));
+#pragma unroll
+                        for (int j = 0; j < NB; ++j) {
+                            const uint32_t at = uint32_t(t + min(j, left - 1) * a.splits);
+                            g[j] += ld_cluster_f32(from + at * 512);
+                            if (GATE) u[j] += ld_cluster_f32(from + (NT + at) * 512);
+                        }
                     }
-                    stream_emit<GATE>(a, t, n, g, u, bg, bu);
+                    stream_emit<EPI, NB>(a, t, a.splits, left, n, g, u, bg, bu);
                 }
             }
         }
@@ -284,10 +326,10 @@ __global__ void __launch_bounds__(kSThreads, 2)
     }
 }
 
-template <bool MX4, bool GATE, int NT>
+template <bool MX4, int EPI, bool WMN, int NT>
 cudaError_t launch_nt(const CUtensorMap& wmap, const CUtensorMap& xmap, const StreamArgs& a, int tiles, cudaStream_t st) {
-    constexpr auto kern = dense_stream_kernel<MX4, GATE, NT>;
-    using C = StreamCfg<MX4, GATE, NT>;
+    constexpr auto kern = dense_stream_kernel<MX4, EPI, WMN, NT>;
+    using C = StreamCfg<MX4, EPI == kEpiGate, NT>;
     cudaError_t e = raise_smem<kern>(C::kSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -296,33 +338,26 @@ cudaError_t launch_nt(const CUtensorMap& wmap, const CUtensorMap& xmap, const St
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
-    int n = 0;
-    if (a.splits > 1) {
-        attr[n].id = cudaLaunchAttributeClusterDimension;
-        attr[n].val.clusterDim.x = unsigned(a.splits);
-        attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
-        ++n;
-    }
-    if (a.after) {
-        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[n].val.programmaticStreamSerializationAllowed = 1;
-        ++n;
-    }
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(a.splits);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = unsigned(n);
+    cfg.numAttrs = a.splits > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, wmap, xmap, a);
 }
 
-template <bool MX4, bool GATE>
+template <bool MX4, int EPI, bool WMN>
 cudaError_t launch_any(const CUtensorMap& wmap, const CUtensorMap& xmap, const StreamArgs& a, int tiles, cudaStream_t st) {
-    if (a.T <= 16) return launch_nt<MX4, GATE, 16>(wmap, xmap, a, tiles, st);
-    if (a.T <= 32) return launch_nt<MX4, GATE, 32>(wmap, xmap, a, tiles, st);
-    return launch_nt<MX4, GATE, 64>(wmap, xmap, a, tiles, st);
+    if (a.T <= 16) return launch_nt<MX4, EPI, WMN, 16>(wmap, xmap, a, tiles, st);
+    if (a.T <= 32) return launch_nt<MX4, EPI, WMN, 32>(wmap, xmap, a, tiles, st);
+    return launch_nt<MX4, EPI, WMN, 64>(wmap, xmap, a, tiles, st);
 }
 
 }  // namespace
 
-cudaError_t launch_dense_stream(const DenseArgs& d, bool after, cudaStream_t st) {
+cudaError_t launch_dense_stream(const DenseArgs& d, bool early_w, cudaStream_t st) {
     const bool gate = d.epi == kEpiGate;
     StreamArgs a{};
     a.T = int(d.M);
@@ -331,12 +366,13 @@ cudaError_t launch_dense_stream(const DenseArgs& d, bool after, cudaStream_t st)
     a.nks = int((d.K + (d.mx4 ? 255 : 63)) / (d.mx4 ? 256 : 64));
     a.out_f32 = d.out_f32;
     a.interleaved = d.interleaved;
-    a.after = after;
+    a.early_w = early_w;
     a.ws = d.b.s;
     a.xs = d.a.s;
     a.bias = d.bias;
     a.out = d.out;
     a.gu = d.gu;
+    a.dgu = (__nv_bfloat16*)d.dgu;
     a.gate = d.gate;
     a.status = d.status;
     a.reset_status = d.reset_status;
@@ -353,15 +389,17 @@ cudaError_t launch_dense_stream(const DenseArgs& d, bool after, cudaStream_t st)
     if (d.mx4) {
         if ((e = encode_map(&wmap, mx4_spec(d.b.p, d.N, d.K, 128))) != cudaSuccess) return e;
         if ((e = encode_map(&xmap, mx4_spec(d.a.p, d.M, d.K, nt))) != cudaSuccess) return e;
-        return launch_any<true, false>(wmap, xmap, a, int(tiles), st);
+        return launch_any<true, kEpiStore, false>(wmap, xmap, a, int(tiles), st);
     }
     if ((e = encode_map(&xmap, bf16_spec(d.a, d.M, d.K, nt, 0))) != cudaSuccess) return e;
     DenseOperand w = d.b;
     if (gate && d.interleaved) w.row *= 2;
     e = encode_map(&wmap, bf16_spec(w, a.N, d.K, 128, !gate ? 0 : d.interleaved ? d.b.row : a.N * d.b.row));
     if (e != cudaSuccess) return e;
-    return gate ? launch_any<false, true>(wmap, xmap, a, int(tiles), st)
-                : launch_any<false, false>(wmap, xmap, a, int(tiles), st);
+    if (gate) return launch_any<false, kEpiGate, false>(wmap, xmap, a, int(tiles), st);
+    if (d.epi == kEpiGateBwd) return launch_any<false, kEpiGateBwd, true>(wmap, xmap, a, int(tiles), st);
+    return d.b.k_step != 1 ? launch_any<false, kEpiStore, true>(wmap, xmap, a, int(tiles), st)
+                           : launch_any<false, kEpiStore, false>(wmap, xmap, a, int(tiles), st);
 }
 
 }  // namespace qmoe

@@ -138,7 +138,7 @@ __device__ __forceinline__ void load_scales(const uint8_t* s, int64_t total, int
 #pragma unroll
         for (int j = 0; j < NW / 4; ++j) {
             uint4 v = make_uint4(0, 0, 0, 0);
-            if (16 * j < n) v = __ldg(reinterpret_cast<const uint4*>(s + at) + j);
+            if (16 * j < n) v = reinterpret_cast<const uint4*>(s + at)[j];
             w[4 * j] = v.x; w[4 * j + 1] = v.y; w[4 * j + 2] = v.z; w[4 * j + 3] = v.w;
         }
         return;
@@ -152,7 +152,7 @@ __device__ __forceinline__ void load_scales(const uint8_t* s, int64_t total, int
         r[j] = 0;
         if (4 * j < n + sh) {
             if (p + 4 <= total) {
-                r[j] = __ldg(reinterpret_cast<const uint32_t*>(s + p));
+                r[j] = *reinterpret_cast<const uint32_t*>(s + p);
             } else {  // the array's last bytes
                 for (int b = 0; b < 4; ++b)
                     if (p + b < total) r[j] |= uint32_t(s[p + b]) << (8 * b);

@@ -61,9 +61,11 @@ __device__ __forceinline__ uint32_t absmax_bits(const uint4& w) {
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads) mx4_quantize_kernel(const uint8_t* __restrict__ x, int64_t rows, int64_t K,
-                                                                int64_t ldb, uint8_t* __restrict__ codes,
-                                                                uint8_t* __restrict__ scales) {
+__global__ void __launch_bounds__(kThreads) mx4_quantize_kernel(const uint8_t* x, int64_t rows, int64_t K,
+                                                                int64_t ldb, uint8_t* codes,
+                                                                uint8_t* scales) {
+    pdl_wait();
+    pdl_trigger();
     constexpr int EV = BF16 ? 8 : 4;            // elements of a vector
     constexpr int LB = 32 / EV;                 // lanes of a block
     constexpr int64_t WE = 32 * EV * kVec;      // elements a warp takes at once
@@ -130,9 +132,11 @@ __device__ __forceinline__ float e2m1_value(uint32_t c) {
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads) mx4_dequantize_kernel(const uint8_t* __restrict__ codes,
-                                                                  const uint8_t* __restrict__ scales, int64_t rows,
-                                                                  int64_t K, uint8_t* __restrict__ x, int64_t ldb) {
+__global__ void __launch_bounds__(kThreads) mx4_dequantize_kernel(const uint8_t* codes,
+                                                                  const uint8_t* scales, int64_t rows,
+                                                                  int64_t K, uint8_t* x, int64_t ldb) {
+    pdl_wait();
+    pdl_trigger();
     constexpr int EV = BF16 ? 8 : 4;
     constexpr int64_t WE = 32 * EV * kVec;
     const int lane = threadIdx.x & 31;
@@ -186,11 +190,8 @@ cudaError_t launch_mx4_quantize(const void* x, int bf16, int64_t rows, int64_t K
     const int64_t ldb = ldx * (bf16 ? 2 : 4);
     if (ldx == K) { K *= rows; rows = 1; }
     const int grid = int(round_grid(rows, K, bf16 ? 8 : 4));
-    if (bf16)
-        mx4_quantize_kernel<true><<<grid, kThreads, 0, st>>>((const uint8_t*)x, rows, K, ldb, codes, scales);
-    else
-        mx4_quantize_kernel<false><<<grid, kThreads, 0, st>>>((const uint8_t*)x, rows, K, ldb, codes, scales);
-    return cudaGetLastError();
+    return launch_kernel(bf16 ? mx4_quantize_kernel<true> : mx4_quantize_kernel<false>, dim3(unsigned(grid)),
+                         dim3(kThreads), 0, st, true, (const uint8_t*)x, rows, K, ldb, codes, scales);
 }
 
 cudaError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K, void* x,
@@ -198,11 +199,8 @@ cudaError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, i
     const int64_t ldb = ldx * (bf16 ? 2 : 4);
     if (ldx == K) { K *= rows; rows = 1; }
     const int grid = int(round_grid(rows, K, bf16 ? 8 : 4));
-    if (bf16)
-        mx4_dequantize_kernel<true><<<grid, kThreads, 0, st>>>(codes, scales, rows, K, (uint8_t*)x, ldb);
-    else
-        mx4_dequantize_kernel<false><<<grid, kThreads, 0, st>>>(codes, scales, rows, K, (uint8_t*)x, ldb);
-    return cudaGetLastError();
+    return launch_kernel(bf16 ? mx4_dequantize_kernel<true> : mx4_dequantize_kernel<false>, dim3(unsigned(grid)),
+                         dim3(kThreads), 0, st, true, codes, scales, rows, K, (uint8_t*)x, ldb);
 }
 
 }  // namespace qmoe
