@@ -49,9 +49,11 @@ template <bool BF16>
 __device__ __forceinline__ uint32_t absmax_bits(const uint4& w) {
     const uint32_t v[4] = {w.x, w.y, w.z, w.w};
     if (BF16) {
-        uint32_t m = 0;
+        __nv_bfloat162 h[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) m = __vmaxu2(m, v[i] & 0x7FFF7FFFu);
+        for (int i = 0; i < 4; ++i) h[i] = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&v[i]));
+        const __nv_bfloat162 q = __hmax2_nan(__hmax2_nan(h[0], h[1]), __hmax2_nan(h[2], h[3]));
+        const uint32_t m = *reinterpret_cast<const uint32_t*>(&q);
         return max(m << 16, m & 0xFFFF0000u);
     }
     uint32_t m = 0;
@@ -60,119 +62,161 @@ __device__ __forceinline__ uint32_t absmax_bits(const uint4& w) {
     return m;
 }
 
+// The chunk of a warp: its row, the lane's first element in it and what is left
+// of the row from there. One long row (every contiguous matrix) needs no
+// division.
+template <int EV>
+__device__ __forceinline__ bool chunk_of(int64_t w, int64_t rows, int64_t K, int64_t& row, int64_t& k0, int& left) {
+    constexpr int64_t WE = 32 * EV * kVec;
+    const int64_t per_row = (K + WE - 1) / WE;
+    if (w >= rows * per_row) return false;
+    row = rows == 1 ? 0 : w / per_row;
+    k0 = (w - row * per_row) * WE + (threadIdx.x & 31) * EV;
+    left = int(min(K - k0, WE));
+    return true;
+}
+
+// Code words and scale byte of a lane's vector.
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads) mx4_quantize_kernel(const uint8_t* x, int64_t rows, int64_t K,
-                                                                int64_t ldb, uint8_t* codes,
-                                                                uint8_t* scales) {
+__device__ __forceinline__ uint32_t quantize_vector(const uint4& v, uint32_t& byte) {
+    constexpr int LB = BF16 ? 4 : 8;  // lanes of a block
+    uint32_t m = absmax_bits<BF16>(v);
+#pragma unroll
+    for (int o = 1; o < LB; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const uint32_t r[4] = {v.x, v.y, v.z, v.w};
+    const bool bad = m >= 0x7F800000u;
+    byte = bad ? 255u : uint32_t(max(int(m >> 23) - 2, 0));
+    uint32_t c;
+    if (BF16) {
+        // 2^(127 - byte) in both halves (anything for a bad block)
+        const uint32_t inv = ((254u - byte) << 7) * 0x00010001u;
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // exact: a power of two, no overflow; what underflows has code 0
+            const __nv_bfloat162 q = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&r[i]),
+                                             *reinterpret_cast<const __nv_bfloat162*>(&inv));
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(&q);
+            f[2 * i] = __uint_as_float(w << 16);
+            f[2 * i + 1] = __uint_as_float(w & 0xFFFF0000u);
+        }
+        c = e2m1x8(f);
+    } else {
+        const float inv = __uint_as_float((254u - byte) << 23);
+        float f[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(r[i]) * inv;
+        c = e2m1x4(f);
+    }
+    return bad ? 0u : c;
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads, 6) mx4_quantize_kernel(const uint8_t* x, int64_t rows, int64_t K, int64_t ldb,
+                                                                   uint8_t* codes, uint8_t* scales) {
     pdl_wait();
     pdl_trigger();
-    constexpr int EV = BF16 ? 8 : 4;            // elements of a vector
-    constexpr int LB = 32 / EV;                 // lanes of a block
-    constexpr int64_t WE = 32 * EV * kVec;      // elements a warp takes at once
-    const int lane = threadIdx.x & 31;
+    constexpr int EV = BF16 ? 8 : 4, ES = 16 / EV, STEP = 32 * EV;  // elements of a vector, bytes, elements of a warp's
     const int64_t nw = int64_t(gridDim.x) * (kThreads / 32);
-    const int64_t per_row = (K + WE - 1) / WE;
-    for (int64_t w = int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); w < rows * per_row; w += nw) {
-        const int64_t row = w / per_row;
-        const int64_t k0 = (w - row * per_row) * WE + lane * EV;
-        const uint8_t* src = x + row * ldb;
+    int64_t row, k0;
+    int left;
+    for (int64_t w = int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); chunk_of<EV>(w, rows, K, row, k0, left);
+         w += nw) {
+        const uint8_t* src = x + row * ldb + k0 * ES;
         uint4 v[kVec];
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-            const int64_t k = k0 + j * 32 * EV;
-            v[j] = k < K ? __ldcs(reinterpret_cast<const uint4*>(src + k * (16 / EV))) : make_uint4(0, 0, 0, 0);
-        }
+        for (int j = 0; j < kVec; ++j)
+            v[j] = j * STEP < left ? __ldcs(reinterpret_cast<const uint4*>(src + j * STEP * ES)) : make_uint4(0, 0, 0, 0);
+        const int64_t at = row * K + k0;
+        uint8_t *cd = codes + at / 2, *sd = scales + at / 32;
+        const bool first = (threadIdx.x & (32 / EV - 1)) == 0;
 #pragma unroll
         for (int j = 0; j < kVec; ++j) {
-            const int64_t k = k0 + j * 32 * EV;
-            uint32_t m = absmax_bits<BF16>(v[j]);
-#pragma unroll
-            for (int o = 1; o < LB; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const bool bad = m >= 0x7F800000u;
-            const int be = int(m >> 23);
-            const uint32_t byte = bad ? 255u : uint32_t(max(be - 2, 0));
-            const float inv = __uint_as_float((254u - byte) << 23);  // 2^(127 - byte); unused when bad
-            const uint32_t r[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
-            uint32_t c;
-            if (BF16) {
-                float f[8];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    f[2 * i] = __uint_as_float(r[i] << 16) * inv;
-                    f[2 * i + 1] = __uint_as_float(r[i] & 0xFFFF0000u) * inv;
-                }
-                c = e2m1x8(f);
-            } else {
-                float f[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(r[i]) * inv;
-                c = e2m1x4(f);
-            }
-            if (bad) c = 0;
-            if (k < K) {
-                uint8_t* d = codes + (row * K + k) / 2;
-                if (BF16) *reinterpret_cast<uint32_t*>(d) = c;
-                else *reinterpret_cast<uint16_t*>(d) = uint16_t(c);
-                if ((lane & (LB - 1)) == 0) scales[(row * K + k) / 32] = uint8_t(byte);
+            uint32_t byte;
+            const uint32_t c = quantize_vector<BF16>(v[j], byte);
+            if (j * STEP < left) {
+                if (BF16) *reinterpret_cast<uint32_t*>(cd + j * STEP / 2) = c;
+                else *reinterpret_cast<uint16_t*>(cd + j * STEP / 2) = uint16_t(c);
+                if (first) sd[j * STEP / 32] = uint8_t(byte);
             }
         }
     }
 }
 
-// 2^(byte - 127); byte 0 is the fp32 subnormal 2^-127, byte 255 is NaN.
-__device__ __forceinline__ float e8m0_value(uint32_t byte) {
-    return __uint_as_float(byte == 0 ? 0x00400000u : byte == 255 ? 0x7FC00000u : byte << 23);
+// 2^(byte - 127) as bf16 bits; byte 0 is the subnormal 2^-127, byte 255 NaN.
+__device__ __forceinline__ uint32_t e8m0_bf16(uint32_t byte) {
+    return byte == 0 ? 0x0040u : byte == 255 ? 0x7FC0u : byte << 7;
 }
 
-// Magnitude by the code's low three bits, twice over: (1 + m/2) 2^(e-1).
-__device__ __forceinline__ float e2m1_value(uint32_t c) {
-    const uint32_t e = (c >> 1) & 3u, m = c & 1u;
-    const float mag = e == 0 ? 0.5f * float(m) : __uint_as_float(((e + 126u) << 23) | (m << 22));
-    return (c & 8u) ? -mag : mag;
+// Four codes (the low 16 bits) to bf16 in order. The values' high and low
+// bytes come from two eight-entry byte tables, four at a time (a byte
+// permute's selectors are the codes' three magnitude bits); the sign comes
+// from the permute's sign mode: of a table of 0x80, a selector with its fourth
+// bit set gives 0xFF and any other 0x80, so bit 0 is the code's sign.
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+    uint32_t r;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
+    return r;
+}
+__device__ __forceinline__ void e2m1x4_to_bf16(uint32_t c, uint32_t& lo, uint32_t& hi) {
+    const uint32_t mag = c & 0x7777u;
+    const uint32_t sign = (prmt(0x80808080u, 0x80808080u, c) & 0x01010101u) << 7;
+    const uint32_t hb = prmt(0x3F3F3F00u, 0x40404040u, mag) | sign;
+    const uint32_t lb = prmt(0xC0800000u, 0xC0804000u, mag);
+    lo = __byte_perm(lb, hb, 0x5140);
+    hi = __byte_perm(lb, hb, 0x7362);
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads) mx4_dequantize_kernel(const uint8_t* codes,
-                                                                  const uint8_t* scales, int64_t rows,
-                                                                  int64_t K, uint8_t* x, int64_t ldb) {
+__global__ void __launch_bounds__(kThreads) mx4_dequantize_kernel(const uint8_t* codes, const uint8_t* scales,
+                                                                  int64_t rows, int64_t K, uint8_t* x, int64_t ldb) {
     pdl_wait();
     pdl_trigger();
-    constexpr int EV = BF16 ? 8 : 4;
-    constexpr int64_t WE = 32 * EV * kVec;
-    const int lane = threadIdx.x & 31;
+    constexpr int EV = BF16 ? 8 : 4, ES = 16 / EV, STEP = 32 * EV;
     const int64_t nw = int64_t(gridDim.x) * (kThreads / 32);
-    const int64_t per_row = (K + WE - 1) / WE;
-    for (int64_t w = int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); w < rows * per_row; w += nw) {
-        const int64_t row = w / per_row;
-        const int64_t k0 = (w - row * per_row) * WE + lane * EV;
+    int64_t row, k0;
+    int left;
+    for (int64_t w = int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); chunk_of<EV>(w, rows, K, row, k0, left);
+         w += nw) {
+        const int64_t at = row * K + k0;
+        const uint8_t *cs = codes + at / 2, *ss = scales + at / 32;
+        uint8_t* dst = x + row * ldb + k0 * ES;
         uint32_t c[kVec], s[kVec];
 #pragma unroll
         for (int j = 0; j < kVec; ++j) {
-            const int64_t k = k0 + j * 32 * EV;
             c[j] = s[j] = 0;
-            if (k < K) {
-                const uint8_t* p = codes + (row * K + k) / 2;
-                c[j] = BF16 ? *reinterpret_cast<const uint32_t*>(p) : *reinterpret_cast<const uint16_t*>(p);
-                s[j] = scales[(row * K + k) / 32];
+            if (j * STEP < left) {
+                c[j] = BF16 ? *reinterpret_cast<const uint32_t*>(cs + j * STEP / 2)
+                            : *reinterpret_cast<const uint16_t*>(cs + j * STEP / 2);
+                s[j] = ss[j * STEP / 32];
             }
         }
 #pragma unroll
         for (int j = 0; j < kVec; ++j) {
-            const int64_t k = k0 + j * 32 * EV;
-            if (k >= K) continue;
-            const float sc = e8m0_value(s[j]);
+            if (j * STEP >= left) break;
+            // a code's value has two significant bits: its product with a power
+            // of two is exact in bf16, subnormals included
             uint32_t o[4];
+            const uint32_t sc = e8m0_bf16(s[j]) * 0x00010001u;
+            if (BF16) {
+                e2m1x4_to_bf16(c[j], o[0], o[1]);
+                e2m1x4_to_bf16(c[j] >> 16, o[2], o[3]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (BF16) {
-                    const __nv_bfloat162 b = __floats2bfloat162_rn(e2m1_value(c[j] >> (8 * i)) * sc,
-                                                                   e2m1_value(c[j] >> (8 * i + 4)) * sc);
+                for (int i = 0; i < 4; ++i) {
+                    const __nv_bfloat162 b = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&o[i]),
+                                                     *reinterpret_cast<const __nv_bfloat162*>(&sc));
                     o[i] = *reinterpret_cast<const uint32_t*>(&b);
-                } else {
-                    o[i] = __float_as_uint(e2m1_value(c[j] >> (4 * i)) * sc);
+                }
+            } else {
+                const float f = __uint_as_float(sc & 0xFFFF0000u);
+                uint32_t v[2];
+                e2m1x4_to_bf16(c[j], v[0], v[1]);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    o[2 * i] = __float_as_uint(__uint_as_float(v[i] << 16) * f);
+                    o[2 * i + 1] = __float_as_uint(__uint_as_float(v[i] & 0xFFFF0000u) * f);
                 }
             }
-            __stcs(reinterpret_cast<uint4*>(x + row * ldb + k * (16 / EV)), make_uint4(o[0], o[1], o[2], o[3]));
+            __stcs(reinterpret_cast<uint4*>(dst + j * STEP * ES), make_uint4(o[0], o[1], o[2], o[3]));
         }
     }
 }
@@ -180,7 +224,7 @@ __global__ void __launch_bounds__(kThreads) mx4_dequantize_kernel(const uint8_t*
 int64_t round_grid(int64_t rows, int64_t K, int ev) {
     const int64_t we = 32 * ev * kVec;
     const int64_t ctas = (rows * ((K + we - 1) / we) + kThreads / 32 - 1) / (kThreads / 32);
-    return ctas < 148 * 16 ? ctas : 148 * 16;
+    return ctas < (1 << 24) ? ctas : (1 << 24);
 }
 
 }  // namespace
