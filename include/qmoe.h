@@ -545,6 +545,16 @@ QMOE_API qmoe_status qmoe_mx4_linear(int64_t T, int64_t N, int64_t K, const uint
                                      size_t workspace_bytes, void* stream);
 
 /*
+ * qmoe_mx4_linear_rows -- the same with x as dense rows [T, K] of dtype, ldx
+ * elements apart: they are rounded as by qmoe_mx4_quantize (whose conditions
+ * on x hold) and multiplied, y = qmoe_mx4_linear of the two.
+ */
+QMOE_API size_t qmoe_mx4_linear_rows_workspace_size(int64_t T, int64_t N, int64_t K);
+QMOE_API qmoe_status qmoe_mx4_linear_rows(int64_t T, int64_t N, int64_t K, const void* x, int64_t ldx,
+                                          const uint8_t* w_codes, const uint8_t* w_scales, const void* bias, void* y,
+                                          int32_t dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Gated feed-forward block, weights dense:
  *   gu = x w1^T + b1   [T, 2I]; swiglu_fusion 1: columns 2i = gate, 2i + 1 =
  *                      up; 2: [0, I) = gate, [I, 2I) = up

@@ -64,11 +64,79 @@ __device__ __forceinline__ float gate_slopes(const GateParams& p, float g, float
     return a * f;
 }
 
+// 4 NW consecutive scales of a row of `pitch` scales, from scale k0 on (a
+// multiple of 4), as words; 0 past the row's end. The array starts on 4 bytes
+// and holds `total` of them; rows need not be aligned, so a row's words are
+// joined from the aligned words that hold them.
+template <int NW>
+__device__ __forceinline__ void load_scales(const uint8_t* s, int64_t total, int64_t row, int64_t pitch, int64_t k0,
+                                            uint32_t (&w)[NW]) {
+    const int64_t at = row * pitch + k0;
+    const int n = int(min(int64_t(4 * NW), max(int64_t(0), pitch - k0)));  // bytes of the row
+    if (NW % 4 == 0 && ((pitch | reinterpret_cast<uintptr_t>(s)) & 15) == 0 && (k0 & 15) == 0) {
+#pragma unroll
+        for (int j = 0; j < NW / 4; ++j) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (16 * j < n) v = reinterpret_cast<const uint4*>(s + at)[j];
+            w[4 * j] = v.x; w[4 * j + 1] = v.y; w[4 * j + 2] = v.z; w[4 * j + 3] = v.w;
+        }
+        return;
+    }
+    const int sh = int(at & 3);
+    const int64_t a0 = at - sh;
+    uint32_t r[NW + 1];
+#pragma unroll
+    for (int j = 0; j <= NW; ++j) {
+        const int64_t p = a0 + 4 * j;
+        r[j] = 0;
+        if (4 * j < n + sh) {
+            if (p + 4 <= total) {
+                r[j] = *reinterpret_cast<const uint32_t*>(s + p);
+            } else {  // the array's last bytes
+                for (int b = 0; b < 4; ++b)
+                    if (p + b < total) r[j] |= uint32_t(s[p + b]) << (8 * b);
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < NW; ++j) {
+        w[j] = __funnelshift_r(r[j], r[j + 1], 8 * sh);
+        const int left = n - 4 * j;
+        if (left < 4) w[j] &= left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+    }
+}
+
+// MX4 scales [rows, K/32] in the order in which the CTA-pair product copies
+// them: [tile of tile_rows rows][chunk of 128 k][ceil(tile_rows / 128)][32][4]
+// words of four scales, the word of row r (in its tile) at lane r % 32, column
+// r / 32 % 4. Rows and scales past the end are 0 (their codes are zero).
+struct ScaleTiles {
+    const uint8_t* s;  // by rows
+    uint8_t* out;      // tiled
+    int64_t rows;
+    int tile_rows, tiles, chunks;
+    __host__ __device__ int subs() const { return (tile_rows + 127) / 128; }
+    __host__ __device__ int64_t threads() const { return int64_t(tiles) * subs() * 128 * ((chunks + 3) / 4); }
+    __host__ __device__ int64_t bytes() const { return int64_t(tiles) * chunks * subs() * 512; }
+    // the byte of a row's scale j; tile_rows is 128 here
+    __device__ int64_t place(int64_t row, int64_t j) const {
+        const int r = int(row & 127);
+        return ((row >> 7) * chunks + (j >> 2)) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (j & 3);
+    }
+};
+
 // ----------------------------------------------------------------- launchers
 cudaError_t launch_mx4_quantize(const void* x, int bf16, int64_t rows, int64_t K, int64_t ldx, uint8_t* codes,
                                 uint8_t* scales, cudaStream_t st);
 cudaError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K, void* x,
                                   int bf16, int64_t ldx, cudaStream_t st);
+
+// Quantise rows of x with their scales tiled (`to`; rows past the end are left
+// as they are: a row's scales enter its own results only), and tile the scales of the product's other operand, in one
+// launch; or tile both operands' scales.
+cudaError_t launch_mx4_quantize_tiled(const void* x, int bf16, int64_t rows, int64_t K, int64_t ldx, uint8_t* codes,
+                                      const ScaleTiles& to, const ScaleTiles& other, cudaStream_t st);
+cudaError_t launch_mx4_tile_scales(const ScaleTiles& a, const ScaleTiles& b, int64_t K, cudaStream_t st);
 
 // One operand of a product: element (r, k) at p + r * row + k * k_step (bf16
 // elements), or MX4 rows (codes p, scales s).
@@ -99,9 +167,12 @@ struct DenseArgs {
     int interleaved;       // gate and up interleaved in w1 / gu (else concatenated)
     int32_t* status;       // workspace status word; reset by the call's first product
     int reset_status;
-    void* scratch;         // mx4: dense_pair_workspace bytes
+    void* scratch;         // mx4: dense_pair_workspace bytes, holding both operands' tiled scales
 };
-size_t dense_pair_workspace(int64_t M, int64_t N, int64_t K);  // re-laid MX4 scales
+// The tiled scales of an MX4 product's operands (their `s` left out) in a
+// scratch of dense_pair_workspace(M, N, K) bytes.
+void dense_pair_tiles(int64_t M, int64_t N, int64_t K, void* scratch, ScaleTiles* a, ScaleTiles* b);
+size_t dense_pair_workspace(int64_t M, int64_t N, int64_t K);
 cudaError_t launch_dense_pair(const DenseArgs& a, cudaStream_t st);
 
 // The same for few rows of A (along k): M up to kStreamRows. early_w: B was not

@@ -130,6 +130,55 @@ cudaError_t launch_rows(const DenseArgs& a, bool early_w, cudaStream_t st) {
     return a.M <= kStreamRows && (a.mx4 || a.a.k_step == 1) ? launch_dense_stream(a, early_w, st) : launch_dense_pair(a, st);
 }
 
+qmoe_status check_linear_sizes(int64_t T, int64_t N, int64_t K) {
+    if (T < 0 || N < 1 || K < 32 || K % 32)
+        return bad(QMOE_INVALID_ARGUMENT, "T >= 0, N >= 1 and K a positive multiple of 32");
+    if (T > kMaxDim || N > kMaxDim || K > kMaxDim) return bad(QMOE_UNSUPPORTED, "T, N or K too large");
+    return QMOE_OK;
+}
+
+qmoe_status check_linear_tensors(const void* w_codes, const void* w_scales, const void* bias, const void* y,
+                                 int32_t dtype) {
+    if (!w_codes || !w_scales || !y) return bad(QMOE_INVALID_ARGUMENT, "w_codes, w_scales and y are required");
+    if (misaligned(w_codes, 16) || misaligned(w_scales, 4))
+        return bad(QMOE_INVALID_ARGUMENT, "codes must be 16-byte, scales 4-byte aligned");
+    const int es = dtype == QMOE_DTYPE_F32 ? 4 : 2;
+    if (misaligned(y, es) || misaligned(bias, es))
+        return bad(QMOE_INVALID_ARGUMENT, "y and bias must be aligned to their elements");
+    return QMOE_OK;
+}
+
+// Tiled scales where the product runs on CTA pairs; the rounded rows of x where
+// the call rounds them (their scales by rows where the product streams).
+struct LinearLayout : Layout {
+    size_t tiles = 0, codes = 0, scales = 0;
+    LinearLayout(int64_t T, int64_t N, int64_t K, bool rows) {
+        if (T > kStreamRows) tiles = take(dense_pair_workspace(T, N, K));
+        if (rows) codes = take(size_t(T) * size_t(K / 2));
+        if (rows) scales = T > kStreamRows ? codes : take(size_t(T) * size_t(K / 32));
+    }
+};
+
+DenseArgs linear_args(int64_t T, int64_t N, int64_t K, const uint8_t* xc, const uint8_t* xs, const uint8_t* wc,
+                      const uint8_t* ws, const void* bias, void* y, int32_t dtype, void* workspace,
+                      const LinearLayout& l) {
+    DenseArgs a{};
+    a.a = {xc, xs, 0, 0};
+    a.b = {wc, ws, 0, 0};
+    a.M = T;
+    a.N = N;
+    a.K = K;
+    a.mx4 = 1;
+    a.epi = kEpiStore;
+    a.out_f32 = dtype == QMOE_DTYPE_F32;
+    a.bias = bias;
+    a.out = y;
+    a.status = (int32_t*)workspace;
+    a.reset_status = 1;
+    a.scratch = T > kStreamRows ? (char*)workspace + l.tiles : nullptr;
+    return a;
+}
+
 DenseOperand rows_of(const void* p, int64_t ld) { return {p, nullptr, ld, 1}; }   // k along the row
 DenseOperand cols_of(const void* p, int64_t ld) { return {p, nullptr, 1, ld}; }   // k across the rows
 
@@ -169,46 +218,68 @@ qmoe_status qmoe_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int
 }
 
 size_t qmoe_mx4_linear_workspace_size(int64_t T, int64_t N, int64_t K) {
-    if (T < 0 || N < 1 || K < 32 || K % 32 || T > kMaxDim || N > kMaxDim || K > kMaxDim) return 0;
-    Layout l;
-    if (T > kStreamRows) l.take(dense_pair_workspace(T, N, K));
-    return l.total;
+    return check_linear_sizes(T, N, K) ? 0 : LinearLayout(T, N, K, false).total;
 }
 
 qmoe_status qmoe_mx4_linear(int64_t T, int64_t N, int64_t K, const uint8_t* x_codes, const uint8_t* x_scales,
                             const uint8_t* w_codes, const uint8_t* w_scales, const void* bias, void* y, int32_t dtype,
                             void* workspace, size_t workspace_bytes, void* stream) {
-    if (T < 0 || N < 1 || K < 32 || K % 32)
-        return bad(QMOE_INVALID_ARGUMENT, "T >= 0, N >= 1 and K a positive multiple of 32");
+    if (qmoe_status s = check_linear_sizes(T, N, K)) return s;
     if (dtype != QMOE_DTYPE_F32 && dtype != QMOE_DTYPE_BF16)
         return bad(QMOE_INVALID_ARGUMENT, "dtype must be F32 or BF16");
-    if (T > kMaxDim || N > kMaxDim || K > kMaxDim) return bad(QMOE_UNSUPPORTED, "T, N or K too large");
     if (T == 0) return QMOE_OK;
-    if (!x_codes || !x_scales || !w_codes || !w_scales || !y)
-        return bad(QMOE_INVALID_ARGUMENT, "codes, scales and y are required");
-    const int es = dtype == QMOE_DTYPE_F32 ? 4 : 2;
-    if (misaligned(x_codes, 16) || misaligned(w_codes, 16) || misaligned(x_scales, 4) || misaligned(w_scales, 4))
-        return bad(QMOE_INVALID_ARGUMENT, "codes must be 16-byte, scales 4-byte aligned");
-    if (misaligned(y, es) || misaligned(bias, es))
-        return bad(QMOE_INVALID_ARGUMENT, "y and bias must be aligned to their elements");
-    if (qmoe_status s = check_workspace(workspace, workspace_bytes, qmoe_mx4_linear_workspace_size(T, N, K))) return s;
+    if (!x_codes || !x_scales || misaligned(x_codes, 16) || misaligned(x_scales, 4))
+        return bad(QMOE_INVALID_ARGUMENT, "x_codes (16-byte) and x_scales (4-byte aligned) are required");
+    if (qmoe_status s = check_linear_tensors(w_codes, w_scales, bias, y, dtype)) return s;
+    const LinearLayout l(T, N, K, false);
+    if (qmoe_status s = check_workspace(workspace, workspace_bytes, l.total)) return s;
     if (qmoe_status s = on_current_device(y)) return s;
-    DenseArgs a{};
-    a.a = {x_codes, x_scales, 0, 0};
-    a.b = {w_codes, w_scales, 0, 0};
-    a.M = T;
-    a.N = N;
-    a.K = K;
-    a.mx4 = 1;
-    a.epi = kEpiStore;
-    a.out_f32 = dtype == QMOE_DTYPE_F32;
-    a.bias = bias;
-    a.out = y;
-    a.status = (int32_t*)workspace;
-    a.reset_status = 1;
-    a.scratch = T > kStreamRows ? (char*)workspace + Layout().total : nullptr;
-    const cudaError_t e = launch_rows(a, false, (cudaStream_t)stream);
+    cudaStream_t st = (cudaStream_t)stream;
+    const DenseArgs a = linear_args(T, N, K, x_codes, x_scales, w_codes, w_scales, bias, y, dtype, workspace, l);
+    cudaError_t e = cudaSuccess;
+    if (a.scratch) {
+        ScaleTiles ta, tb;
+        dense_pair_tiles(T, N, K, a.scratch, &ta, &tb);
+        ta.s = x_scales;
+        tb.s = w_scales;
+        e = launch_mx4_tile_scales(ta, tb, K, st);
+    }
+    if (e == cudaSuccess) e = launch_rows(a, false, st);
     return e == cudaSuccess ? QMOE_OK : cuda_bad(e, "mx4_linear");
+}
+
+size_t qmoe_mx4_linear_rows_workspace_size(int64_t T, int64_t N, int64_t K) {
+    return check_linear_sizes(T, N, K) ? 0 : LinearLayout(T, N, K, true).total;
+}
+
+qmoe_status qmoe_mx4_linear_rows(int64_t T, int64_t N, int64_t K, const void* x, int64_t ldx, const uint8_t* w_codes,
+                                 const uint8_t* w_scales, const void* bias, void* y, int32_t dtype, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+    if (qmoe_status s = check_linear_sizes(T, N, K)) return s;
+    const LinearLayout l(T, N, K, true);
+    uint8_t* codes = (uint8_t*)workspace + l.codes;
+    uint8_t* scales = (uint8_t*)workspace + l.scales;
+    if (T > 0)
+        if (qmoe_status s = check_workspace(workspace, workspace_bytes, l.total)) return s;
+    if (qmoe_status s = check_mx4_rows(x, dtype, T, K, ldx, codes, scales)) return s;
+    if (T == 0) return QMOE_OK;
+    if (qmoe_status s = check_linear_tensors(w_codes, w_scales, bias, y, dtype)) return s;
+    if (qmoe_status s = on_current_device(y)) return s;
+    cudaStream_t st = (cudaStream_t)stream;
+    const int bf16 = dtype == QMOE_DTYPE_BF16;
+    const int64_t ld = T > 1 ? ldx : K;
+    const DenseArgs a = linear_args(T, N, K, codes, scales, w_codes, w_scales, bias, y, dtype, workspace, l);
+    cudaError_t e;
+    if (a.scratch) {
+        ScaleTiles ta, tb;
+        dense_pair_tiles(T, N, K, a.scratch, &ta, &tb);
+        tb.s = w_scales;
+        e = launch_mx4_quantize_tiled(x, bf16, T, K, ld, codes, ta, tb, st);
+    } else {
+        e = launch_mx4_quantize(x, bf16, T, K, ld, codes, scales, st);
+    }
+    if (e == cudaSuccess) e = launch_rows(a, true, st);  // the rounding wrote none of the weights
+    return e == cudaSuccess ? QMOE_OK : cuda_bad(e, "mx4_linear_rows");
 }
 
 size_t qmoe_gated_ffn_workspace_size(const qmoe_gated_ffn_config* cfg, int64_t T, int32_t backward) {

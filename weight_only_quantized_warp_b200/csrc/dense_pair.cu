@@ -17,7 +17,7 @@
 //
 // kind::mxf4 (MX4): products of e2m1 values with both E8M0 scales applied by
 // the tensor core, two scales per row and MMA (64 k). Scales are copied with
-// each stage from a re-laid array (see mx4_tile_scales_kernel) and from shared
+// each stage from an array tiled beforehand (ScaleTiles) and from shared
 // to tensor memory by tcgen05.cp ahead of the stage's MMAs. BN is 240, not
 // 256: two 240-column accumulators leave 32 columns for a stage's scales.
 //
@@ -427,40 +427,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
     }
 }
 
-// MX4 scales [rows, K/32] to the order in which the product copies them:
-// [tile of tr rows][128-k chunk][ceil(tr/128)][32][4] words of four scales, the
-// word of row r (in its tile) and chunk c at lane r % 32, column r / 32 % 4.
-// Rows and scales past the end are 0 (their codes are zero).
-__global__ void __launch_bounds__(256) mx4_tile_scales_kernel(const uint8_t* sa, int64_t rows_a, int tr_a, int tiles_a,
-                                                              uint32_t* oa, const uint8_t* sb, int64_t rows_b,
-                                                              int tr_b, int tiles_b, uint32_t* ob, int64_t pitch,
-                                                              int chunks) {
-    pdl_wait();
-    pdl_trigger();
-    const bool second = blockIdx.y == 1;
-    const uint8_t* s = second ? sb : sa;
-    const int64_t rows = second ? rows_b : rows_a;
-    const int tr = second ? tr_b : tr_a, tiles = second ? tiles_b : tiles_a, subs = (tr + 127) / 128;
-    uint32_t* o = second ? ob : oa;
-    const int groups = (chunks + 3) / 4;  // 16 scales of a row
-    const int64_t total = int64_t(tiles) * subs * 128 * groups;
-    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < total; i += int64_t(gridDim.x) * 256) {
-        const int64_t pr = i / groups;  // padded row
-        const int g = int(i - pr * groups);
-        const int64_t tile = pr / (subs * 128);
-        const int r = int(pr - tile * subs * 128);
-        const int64_t row = tile * tr + r;
-        uint32_t w[4] = {0, 0, 0, 0};
-        if (r < tr && row < rows) load_scales<4>(s, rows * pitch, row, pitch, g * 16, w);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int c = g * 4 + j;
-            if (c < chunks)
-                o[((tile * chunks + c) * subs + (r >> 7)) * 128 + (r & 31) * 4 + ((r >> 5) & 3)] = w[j];
-        }
-    }
-}
-
 template <bool MX4, bool AMN, bool BMN, int EPI>
 cudaError_t launch_one(const CUtensorMap (&maps)[4], const PairArgs& a, cudaStream_t st) {
     constexpr auto kern = dense_pair_kernel<MX4, AMN, BMN, EPI>;
@@ -498,9 +464,16 @@ int64_t up256(int64_t v) { return (v + 255) & ~int64_t(255); }
 
 }  // namespace
 
+void dense_pair_tiles(int64_t M, int64_t N, int64_t K, void* scratch, ScaleTiles* a, ScaleTiles* b) {
+    const int BN = PairCfg<true>::BN;
+    *a = {nullptr, (uint8_t*)scratch, M, 128, int((M + 255) / 256) * 2, int(pair_chunks(K))};
+    *b = {nullptr, (uint8_t*)scratch + up256(a->bytes()), N, BN, int((N + BN - 1) / BN), a->chunks};
+}
+
 size_t dense_pair_workspace(int64_t M, int64_t N, int64_t K) {
-    const int64_t c = pair_chunks(K);
-    return size_t(up256(((M + 255) / 256) * 2 * c * 512) + up256(((N + 239) / 240) * c * 1024));
+    ScaleTiles a, b;
+    dense_pair_tiles(M, N, K, nullptr, &a, &b);
+    return size_t(up256(a.bytes()) + up256(b.bytes()));
 }
 
 cudaError_t launch_dense_pair(const DenseArgs& d, cudaStream_t st) {
@@ -531,24 +504,17 @@ cudaError_t launch_dense_pair(const DenseArgs& d, cudaStream_t st) {
     cudaError_t e;
     if (d.mx4) {
         if (!d.scratch) return cudaErrorInvalidValue;
-        const int64_t c = pair_chunks(d.K), ta = int64_t(a.tiles_m) * 2, tb = a.tiles_n;
-        a.chunks = int(c);
-        uint8_t* oa = (uint8_t*)d.scratch;
-        uint8_t* ob = oa + up256(ta * c * 512);
-        const int64_t words = (ta > 2 * tb ? ta : 2 * tb) * 128 * ((c + 3) / 4);
-        const int64_t blocks = (words + 255) / 256;
-        e = launch_kernel(mx4_tile_scales_kernel, dim3(unsigned(blocks < 4096 ? blocks : 4096), 2), dim3(256), 0, st, true,
-                          d.a.s, d.M, 128, int(ta), (uint32_t*)oa, d.b.s, d.N, BN, int(tb), (uint32_t*)ob, d.K / 32,
-                          int(c));
-        if (e != cudaSuccess) return e;
+        ScaleTiles t[2];
+        dense_pair_tiles(d.M, d.N, d.K, d.scratch, &t[0], &t[1]);
+        a.chunks = t[0].chunks;
         for (int i = 0; i < 2; ++i) {
             const MapSpec s = i ? mx4_spec(d.b.p, d.N, d.K, uint32_t(BN / 2)) : mx4_spec(d.a.p, d.M, d.K, 128);
             if ((e = encode_map(&maps[i], s)) != cudaSuccess) return e;
             MapSpec sc{};
-            sc.p = i ? ob : oa;
+            sc.p = t[i].out;
             sc.type = CU_TENSOR_MAP_DATA_TYPE_INT32;
             sc.dims[0] = 256;
-            sc.dims[1] = uint64_t(i ? tb * c : ta * c / 2);
+            sc.dims[1] = uint64_t(t[i].bytes() / 1024);
             sc.dims[2] = 1;
             sc.strides[0] = sc.strides[1] = 1024;
             sc.box[0] = 256;

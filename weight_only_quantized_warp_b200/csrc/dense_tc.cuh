@@ -125,48 +125,6 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
     return v;
 }
 
-// 4 NW consecutive scales of a row of `pitch` scales, from scale k0 on (a
-// multiple of 4), as words; 0 past the row's end. The array starts on 4 bytes
-// and holds `total` of them; rows need not be aligned, so a row's words are
-// joined from the aligned words that hold them.
-template <int NW>
-__device__ __forceinline__ void load_scales(const uint8_t* s, int64_t total, int64_t row, int64_t pitch, int64_t k0,
-                                            uint32_t (&w)[NW]) {
-    const int64_t at = row * pitch + k0;
-    const int n = int(min(int64_t(4 * NW), max(int64_t(0), pitch - k0)));  // bytes of the row
-    if (NW % 4 == 0 && ((pitch | reinterpret_cast<uintptr_t>(s)) & 15) == 0 && (k0 & 15) == 0) {
-#pragma unroll
-        for (int j = 0; j < NW / 4; ++j) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (16 * j < n) v = reinterpret_cast<const uint4*>(s + at)[j];
-            w[4 * j] = v.x; w[4 * j + 1] = v.y; w[4 * j + 2] = v.z; w[4 * j + 3] = v.w;
-        }
-        return;
-    }
-    const int sh = int(at & 3);
-    const int64_t a0 = at - sh;
-    uint32_t r[NW + 1];
-#pragma unroll
-    for (int j = 0; j <= NW; ++j) {
-        const int64_t p = a0 + 4 * j;
-        r[j] = 0;
-        if (4 * j < n + sh) {
-            if (p + 4 <= total) {
-                r[j] = *reinterpret_cast<const uint32_t*>(s + p);
-            } else {  // the array's last bytes
-                for (int b = 0; b < 4; ++b)
-                    if (p + b < total) r[j] |= uint32_t(s[p + b]) << (8 * b);
-            }
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < NW; ++j) {
-        w[j] = __funnelshift_r(r[j], r[j + 1], 8 * sh);
-        const int left = n - 4 * j;
-        if (left < 4) w[j] &= left <= 0 ? 0u : (1u << (8 * left)) - 1u;
-    }
-}
-
 // Shared-memory descriptor of an operand whose rows (M or N) lie along
 // 128-byte swizzled lines of 64 bf16, one line per k: 64-row chunks 8192 bytes
 // apart (64 k each), groups of 8 k 1024 bytes apart.
@@ -220,10 +178,14 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 
 // ---------------------------------------------------------------- host side
 
+// Multiprocessors of the current device (looked up once per device).
 inline int sm_count() {
-    int dev = 0, sms = 148;
+    static std::atomic<int> known[64];
+    int dev = 0, sms = 0;
     cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (dev < 64 && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 2) return 148;
+    if (dev < 64) known[dev].store(sms, std::memory_order_relaxed);
     return sms;
 }
 

@@ -14,7 +14,7 @@
 // (a block is 4 lanes of bf16 or 8 of fp32, joined by shuffles), kVec of them
 // in flight; a row that continues in the next (ldx = K) is walked as one long
 // row.
-#include "qmoe_internal.cuh"
+#include "dense.cuh"
 
 namespace qmoe {
 namespace {
@@ -110,22 +110,61 @@ __device__ __forceinline__ uint32_t quantize_vector(const uint4& v, uint32_t& by
     return bad ? 0u : c;
 }
 
-template <bool BF16>
-__global__ void __launch_bounds__(kThreads, 6) mx4_quantize_kernel(const uint8_t* x, int64_t rows, int64_t K, int64_t ldb,
-                                                                   uint8_t* codes, uint8_t* scales) {
+__device__ __forceinline__ void tile_scales(const ScaleTiles& t, int64_t pitch, int64_t i, int64_t step) {
+    const int subs = t.subs(), groups = (t.chunks + 3) / 4;  // 16 scales of a row
+    const int64_t total = t.threads();
+    for (; i < total; i += step) {
+        const int64_t pr = i / groups;  // padded row
+        const int g = int(i - pr * groups);
+        const int64_t tile = pr / (subs * 128);
+        const int r = int(pr - tile * subs * 128);
+        const int64_t row = tile * t.tile_rows + r;
+        uint32_t w[4] = {0, 0, 0, 0};
+        if (r < t.tile_rows && row < t.rows) load_scales<4>(t.s, t.rows * pitch, row, pitch, g * 16, w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int c = g * 4 + j;
+            if (c < t.chunks)
+                reinterpret_cast<uint32_t*>(t.out)[((tile * t.chunks + c) * subs + (r >> 7)) * 128 + (r & 31) * 4 +
+                                                   ((r >> 5) & 3)] = w[j];
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kThreads) mx4_tile_scales_kernel(const ScaleTiles a, const ScaleTiles b, int64_t pitch) {
     pdl_wait();
     pdl_trigger();
+    tile_scales(blockIdx.y == 0 ? a : b, pitch, int64_t(blockIdx.x) * kThreads + threadIdx.x,
+                int64_t(gridDim.x) * kThreads);
+}
+
+// TILED: the scales go to the order of the product's copies instead of rows,
+// and the CTAs from `own` on lay out the other operand's scales (the work of
+// one more launch).
+template <bool BF16, bool TILED>
+__global__ void __launch_bounds__(kThreads, 6) mx4_quantize_kernel(const uint8_t* x, int64_t rows, int64_t K, int64_t ldb,
+                                                                   uint8_t* codes, uint8_t* scales, int own,
+                                                                   const ScaleTiles to, const ScaleTiles other) {
+    pdl_wait();
+    pdl_trigger();
+    if (TILED && int(blockIdx.x) >= own) {
+        tile_scales(other, K / 32, int64_t(blockIdx.x - own) * kThreads + threadIdx.x,
+                    int64_t(gridDim.x - own) * kThreads);
+        return;
+    }
     constexpr int EV = BF16 ? 8 : 4, ES = 16 / EV, STEP = 32 * EV;  // elements of a vector, bytes, elements of a warp's
-    const int64_t nw = int64_t(gridDim.x) * (kThreads / 32);
+    const int64_t nw = int64_t(own) * (kThreads / 32);
+    const int64_t KW = TILED ? int64_t(to.chunks) * 128 : K;  // tiled scales end on a stage: zeros after K
     int64_t row, k0;
     int left;
-    for (int64_t w = int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); chunk_of<EV>(w, rows, K, row, k0, left);
+    for (int64_t w = int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); chunk_of<EV>(w, rows, KW, row, k0, left);
          w += nw) {
         const uint8_t* src = x + row * ldb + k0 * ES;
+        const int have = TILED ? int(min(K - k0, int64_t(left))) : left;
         uint4 v[kVec];
 #pragma unroll
         for (int j = 0; j < kVec; ++j)
-            v[j] = j * STEP < left ? __ldcs(reinterpret_cast<const uint4*>(src + j * STEP * ES)) : make_uint4(0, 0, 0, 0);
+            v[j] = j * STEP < have ? __ldcs(reinterpret_cast<const uint4*>(src + j * STEP * ES)) : make_uint4(0, 0, 0, 0);
         const int64_t at = row * K + k0;
         uint8_t *cd = codes + at / 2, *sd = scales + at / 32;
         const bool first = (threadIdx.x & (32 / EV - 1)) == 0;
@@ -133,10 +172,13 @@ __global__ void __launch_bounds__(kThreads, 6) mx4_quantize_kernel(const uint8_t
         for (int j = 0; j < kVec; ++j) {
             uint32_t byte;
             const uint32_t c = quantize_vector<BF16>(v[j], byte);
-            if (j * STEP < left) {
+            if (j * STEP < have) {
                 if (BF16) *reinterpret_cast<uint32_t*>(cd + j * STEP / 2) = c;
                 else *reinterpret_cast<uint16_t*>(cd + j * STEP / 2) = uint16_t(c);
-                if (first) sd[j * STEP / 32] = uint8_t(byte);
+            }
+            if (first && j * STEP < left) {
+                if (TILED) to.out[to.place(row, (k0 + j * STEP) / 32)] = uint8_t(byte);
+                else sd[j * STEP / 32] = uint8_t(byte);
             }
         }
     }
@@ -234,8 +276,25 @@ cudaError_t launch_mx4_quantize(const void* x, int bf16, int64_t rows, int64_t K
     const int64_t ldb = ldx * (bf16 ? 2 : 4);
     if (ldx == K) { K *= rows; rows = 1; }
     const int grid = int(round_grid(rows, K, bf16 ? 8 : 4));
-    return launch_kernel(bf16 ? mx4_quantize_kernel<true> : mx4_quantize_kernel<false>, dim3(unsigned(grid)),
-                         dim3(kThreads), 0, st, true, (const uint8_t*)x, rows, K, ldb, codes, scales);
+    return launch_kernel(bf16 ? mx4_quantize_kernel<true, false> : mx4_quantize_kernel<false, false>, dim3(unsigned(grid)),
+                         dim3(kThreads), 0, st, true, (const uint8_t*)x, rows, K, ldb, codes, scales, grid, ScaleTiles{},
+                         ScaleTiles{});
+}
+
+cudaError_t launch_mx4_quantize_tiled(const void* x, int bf16, int64_t rows, int64_t K, int64_t ldx, uint8_t* codes,
+                                      const ScaleTiles& to, const ScaleTiles& other, cudaStream_t st) {
+    const int grid = int(round_grid(rows, int64_t(to.chunks) * 128, bf16 ? 8 : 4));
+    const int64_t blocks = (other.threads() + kThreads - 1) / kThreads;
+    const int more = int(blocks < 4096 ? blocks : 4096);
+    return launch_kernel(bf16 ? mx4_quantize_kernel<true, true> : mx4_quantize_kernel<false, true>,
+                         dim3(unsigned(grid + more)), dim3(kThreads), 0, st, true, (const uint8_t*)x, rows, K,
+                         ldx * (bf16 ? 2 : 4), codes, (uint8_t*)nullptr, grid, to, other);
+}
+
+cudaError_t launch_mx4_tile_scales(const ScaleTiles& a, const ScaleTiles& b, int64_t K, cudaStream_t st) {
+    const int64_t t = a.threads() > b.threads() ? a.threads() : b.threads(), blocks = (t + kThreads - 1) / kThreads;
+    return launch_kernel(mx4_tile_scales_kernel, dim3(unsigned(blocks < 4096 ? blocks : 4096), 2), dim3(kThreads), 0, st,
+                         true, a, b, K / 32);
 }
 
 cudaError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K, void* x,

@@ -61,6 +61,20 @@ def _address(t):
     return None if t is None else t.data_ptr()
 
 
+def _rows(x):
+    """``(x, ldx)``: a 2-D x with unit stride along K and 16-byte aligned rows as
+    it lies, any other layout through a contiguous copy."""
+    ldx = x.shape[-1]
+    if not x.is_contiguous():
+        if x.dim() == 2 and x.stride(1) == 1 and x.stride(0) >= ldx and x.stride(0) * x.element_size() % 16 == 0:
+            ldx = x.stride(0)
+        else:
+            x = x.contiguous()
+    if x.data_ptr() % 16:
+        x, ldx = x.clone(memory_format=torch.contiguous_format), x.shape[-1]
+    return x, ldx
+
+
 def mx4_quantize(x):
     """x [..., K] (float32 or bfloat16, K a multiple of 32) to ``(codes, scales)``:
     uint8 [..., K/2] and [..., K/32]. A 2-D x with unit stride along K and
@@ -71,14 +85,7 @@ def mx4_quantize(x):
     if not shape or shape[-1] < MX4_BLOCK or shape[-1] % MX4_BLOCK:
         raise ValueError(f"the last dimension must be a positive multiple of {MX4_BLOCK}")
     index, K = _gpu(x, "x"), shape[-1]
-    ldx = K
-    if not x.is_contiguous():
-        if x.dim() == 2 and x.stride(1) == 1 and x.stride(0) >= K and x.stride(0) * x.element_size() % 16 == 0:
-            ldx = x.stride(0)
-        else:
-            x = x.contiguous()
-    if x.data_ptr() % 16:
-        x, ldx = x.clone(memory_format=torch.contiguous_format), K
+    x, ldx = _rows(x)
     lead = shape[:-1]
     codes = x.new_empty((*lead, K // 2), dtype=torch.uint8)
     scales = x.new_empty((*lead, K // MX4_BLOCK), dtype=torch.uint8)
@@ -136,14 +143,17 @@ def mx4_linear(x_codes, x_scales, w_codes, w_scales, bias=None, dtype=torch.bflo
 
 
 class MX4Linear:
-    """A linear layer kept in 4 bits: ``layer(x)`` quantises x's rows and
-    multiplies. Weights come as MX4 rows [N, K/2], [N, K/32], or dense through
-    ``from_weights``."""
+    """A linear layer kept in 4 bits: ``layer(x)`` rounds x's rows to MX4 and
+    multiplies; the output has x's dtype, which the bias must have too. Weights
+    come as MX4 rows [N, K/2], [N, K/32], or dense through ``from_weights``."""
 
     def __init__(self, w_codes, w_scales, bias=None):
-        _check_mx4(w_codes, w_scales, "w_")
-        if w_codes.dim() != 2:
-            raise ValueError("w_codes must be [N, K/2]")
+        self.in_features = _check_mx4(w_codes, w_scales, "w_")
+        if w_codes.dim() != 2 or not w_codes.shape[0]:
+            raise ValueError(f"w_codes must be [N, K/2], not {tuple(w_codes.shape)}")
+        self.out_features = w_codes.shape[0]
+        if bias is not None:
+            _tensor(bias, "bias", (self.out_features,), bias.dtype, w_codes.get_device())
         self.w_codes, self.w_scales, self.bias = w_codes, w_scales, bias
 
     @classmethod
@@ -151,8 +161,21 @@ class MX4Linear:
         return cls(*mx4_quantize(w), bias)
 
     def forward(self, x):
-        codes, scales = mx4_quantize(x)
-        return mx4_linear(codes, scales, self.w_codes, self.w_scales, self.bias, x.dtype)
+        code, shape, K, N, bias = _dtype_code(x.dtype), x.shape, self.in_features, self.out_features, self.bias
+        index = _gpu(x, "x")
+        if not shape or shape[-1] != K or self.w_codes.get_device() != index:
+            raise ValueError(f"x must be [..., {K}] on {self.w_codes.device}, not {tuple(shape)} on {x.device}")
+        if bias is not None and bias.dtype != x.dtype:
+            raise ValueError(f"the bias is {bias.dtype}, x is {x.dtype}")
+        x, ldx = _rows(x)
+        y = x.new_empty((*shape[:-1], N))
+        T = x.numel() // K
+        if T:
+            n = qmoe.lib.qmoe_mx4_linear_rows_workspace_size(T, N, K)
+            ws = x.new_empty(n, dtype=torch.uint8)
+            _enqueue(index, qmoe.lib.qmoe_mx4_linear_rows, T, N, K, x.data_ptr(), ldx, self.w_codes.data_ptr(),
+                     self.w_scales.data_ptr(), _address(bias), y.data_ptr(), code, ws.data_ptr(), n)
+        return y
 
     __call__ = forward
 

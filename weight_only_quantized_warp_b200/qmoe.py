@@ -45,6 +45,7 @@ EXPORTS = ("qmoe_create", "qmoe_set_weights", "qmoe_workspace_size", "qmoe_forwa
            "qmoe_ep_rows_workspace_size", "qmoe_ep_expert_rows", "qmoe_ep_combine",
            "qmoe_dense_last_error", "qmoe_dense_read_device_status", "qmoe_mx4_quantize",
            "qmoe_mx4_dequantize", "qmoe_mx4_linear_workspace_size", "qmoe_mx4_linear",
+           "qmoe_mx4_linear_rows_workspace_size", "qmoe_mx4_linear_rows",
            "qmoe_gated_ffn_workspace_size", "qmoe_gated_ffn_forward", "qmoe_gated_ffn_backward")
 QMOE_OPT_PATH, QMOE_OPT_WAIT_LIMIT_NS, QMOE_OPT_TEST_WITHHOLD, QMOE_OPT_PDL, QMOE_OPT_DECODE_TILES = 1, 2, 3, 4, 5
 
@@ -140,6 +141,10 @@ lib.qmoe_mx4_linear_workspace_size.restype = _sz
 lib.qmoe_mx4_linear_workspace_size.argtypes = [_i64, _i64, _i64]
 lib.qmoe_mx4_linear.restype = ctypes.c_int
 lib.qmoe_mx4_linear.argtypes = [_i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _sz, _vp]
+lib.qmoe_mx4_linear_rows_workspace_size.restype = _sz
+lib.qmoe_mx4_linear_rows_workspace_size.argtypes = [_i64, _i64, _i64]
+lib.qmoe_mx4_linear_rows.restype = ctypes.c_int
+lib.qmoe_mx4_linear_rows.argtypes = [_i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i32, _vp, _sz, _vp]
 lib.qmoe_gated_ffn_workspace_size.restype = _sz
 lib.qmoe_gated_ffn_workspace_size.argtypes = [_ffn, _i64, _i32]
 lib.qmoe_gated_ffn_forward.restype = ctypes.c_int
@@ -353,6 +358,16 @@ def qmoe_mx4_linear(T, N, K, x_codes, x_scales, w_codes, w_scales, bias, y, dtyp
                     stream=None):
     _check_dense(lib.qmoe_mx4_linear(T, N, K, _ptr(x_codes), _ptr(x_scales), _ptr(w_codes), _ptr(w_scales),
                                      _ptr(bias), _ptr(y), dtype, _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def qmoe_mx4_linear_rows_workspace_size(T: int, N: int, K: int) -> int:
+    return int(lib.qmoe_mx4_linear_rows_workspace_size(T, N, K))
+
+
+def qmoe_mx4_linear_rows(T, N, K, x, ldx, w_codes, w_scales, bias, y, dtype, workspace, workspace_bytes, stream=None):
+    """The product with x as dense rows, rounded to MX4 in the call."""
+    _check_dense(lib.qmoe_mx4_linear_rows(T, N, K, _ptr(x), ldx, _ptr(w_codes), _ptr(w_scales), _ptr(bias), _ptr(y),
+                                          dtype, _ptr(workspace), workspace_bytes, _stream(stream)))
 
 
 def qmoe_gated_ffn_workspace_size(cfg: qmoe_gated_ffn_config, T: int, backward: bool) -> int:
