@@ -34,7 +34,7 @@ namespace {
 
 constexpr int kPThreads = 384;
 constexpr int kPEpi0 = 4, kPEpiWarps = 8;
-constexpr int kGroupM = 8;
+constexpr int kGroupM = 8;  // 2, 4 and 16 measured the same
 constexpr int kABytes = 128 * 128;  // one CTA's A rows of a stage
 
 struct PairArgs {
@@ -71,85 +71,91 @@ __device__ __forceinline__ void pair_tile(const PairArgs& a, int t, int& tm, int
     tn = r / gm;
 }
 
-// 32 accumulator columns of the warp's lanes, of which `left` belong to the
-// tile (16 at least: the rest is not read).
-__device__ __forceinline__ void tmem_f32(uint32_t t, int left, float (&v)[32]) {
-    if (left >= 32) {
-        uint32_t r[32];
-        tmem_ld32(t, r);
-        tmem_wait_ld();
+// 32 accumulator columns of the warp's lanes (columns past the tile's are read
+// too, inside the allocation, and not used).
+__device__ __forceinline__ void tmem_f32(uint32_t t, float (&v)[32]) {
+    uint32_t r[32];
+    tmem_ld32(t, r);
+    tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-    } else {
-        float w[16];
-        tmem_ld16(t, w);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = i < 16 ? w[i & 15] : 0.0f;
-    }
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// Turn of a 32 x 32 block through a warp's 4 KB: in tensor memory a lane holds
-// a row, in global memory a row wants neighbouring lanes. Lane r writes its
-// row as 16 pairs, pair j at place j ^ (r & 15) of its line (no bank
-// conflicts either way); then half warps read one row each, lane p of a half
-// its pair p.
-__device__ __forceinline__ void turn_put(float2* buf, int lane, const float (&v)[32]) {
+// Turn of a block of 32 rows through a warp's 4 KB: in tensor memory a lane
+// holds a row, in global memory a row wants neighbouring lanes. A row is NU
+// units of 16 bytes (8: 32 fp32 or 64 bf16 columns; 4: 32 bf16). Lane r writes
+// row r; then NU lanes read a row's units and 32 / NU rows go out in one
+// instruction. Unit j of row r lies at place j ^ (r NU / 8 mod NU) of its line:
+// eight neighbouring lanes hit eight different 16-byte banks both ways.
+template <int NU>
+__device__ __forceinline__ int turn_at(int row, int j) {
+    return row * NU + (j ^ ((row * NU / 8) & (NU - 1)));
+}
+template <int NU>
+__device__ __forceinline__ void turn_put(uint4* buf, int lane, const uint4 (&v)[NU]) {
     __syncwarp();
 #pragma unroll
-    for (int j = 0; j < 16; ++j) buf[lane * 16 + (j ^ (lane & 15))] = make_float2(v[2 * j], v[2 * j + 1]);
+    for (int j = 0; j < NU; ++j) buf[turn_at<NU>(lane, j)] = v[j];
     __syncwarp();
 }
-__device__ __forceinline__ float2 turn_get(const float2* buf, int row, int p) { return buf[row * 16 + (p ^ (row & 15))]; }
-
-__device__ __forceinline__ void store_pair(__nv_bfloat16* p, float2 v, bool two, bool vec) {
-    if (two && vec) {
-        *reinterpret_cast<uint32_t*>(p) = pack_bf16(v.x, v.y);
-    } else {
-        p[0] = __float2bfloat16_rn(v.x);
-        if (two) p[1] = __float2bfloat16_rn(v.y);
-    }
+__device__ __forceinline__ void put_f32(uint4* buf, int lane, const float (&v)[32]) {
+    uint4 w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        w[j] = make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]), __float_as_uint(v[4 * j + 2]),
+                          __float_as_uint(v[4 * j + 3]));
+    turn_put<8>(buf, lane, w);
 }
-__device__ __forceinline__ void store_pair(float* p, float2 v, bool two, bool vec) {
-    if (two && vec) {
-        *reinterpret_cast<float2*>(p) = v;
-    } else {
-        p[0] = v.x;
-        if (two) p[1] = v.y;
+__device__ __forceinline__ void pack32(const float (&v)[32], uint4* w) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        w[j] = make_uint4(pack_bf16(v[8 * j], v[8 * j + 1]), pack_bf16(v[8 * j + 2], v[8 * j + 3]),
+                          pack_bf16(v[8 * j + 4], v[8 * j + 5]), pack_bf16(v[8 * j + 6], v[8 * j + 7]));
+}
+
+// A turned block to rows of `ld` elements: `rows` of its rows, `cols` of its
+// columns; out is at its first element. vec: rows start on 16 bytes.
+// Otherwise lanes take words of a row, as whole words where those are aligned.
+template <int NU, typename T>
+__device__ __forceinline__ void turn_out(const uint4* buf, T* out, int64_t ld, int rows, int cols, bool vec, int lane) {
+    constexpr int E = 16 / int(sizeof(T)), RI = 32 / NU;
+    if (vec) {
+        const int j = lane % NU, r0 = lane / NU;
+        T* o = out + r0 * ld + j * E;
+        const bool mine = j * E < cols;  // cols is a multiple of E where rows are aligned
+        uint4 v[NU];
+#pragma unroll
+        for (int i = 0; i < NU; ++i) v[i] = buf[turn_at<NU>(i * RI + r0, j)];
+#pragma unroll
+        for (int i = 0; i < NU; ++i) {
+            if (mine && i * RI + r0 < rows) *reinterpret_cast<uint4*>(o) = v[i];
+            o += RI * ld;
+        }
+        return;
     }
+    const uint32_t* words = reinterpret_cast<const uint32_t*>(buf);
+    constexpr int EW = 4 / int(sizeof(T));  // elements of a word
+    const bool whole = EW == 1 || (((reinterpret_cast<uintptr_t>(out) & 3) == 0) && ld % 2 == 0);
+    for (int r = 0; r < rows; ++r)
+        for (int w = lane; w < NU * 4; w += 32) {
+            const uint32_t v = words[turn_at<NU>(r, w >> 2) * 4 + (w & 3)];
+            T* o = out + r * ld + w * EW;
+            if (w * EW + EW <= cols && whole) {
+                *reinterpret_cast<uint32_t*>(o) = v;
+            } else if (EW == 2) {
+                if (2 * w < cols) reinterpret_cast<uint16_t*>(o)[0] = uint16_t(v);
+                if (2 * w + 1 < cols) reinterpret_cast<uint16_t*>(o)[1] = uint16_t(v >> 16);
+            }
+        }
 }
 
 // Loads that stay where they are written, ahead of the arithmetic: a batch of
 // them covers one latency.
-__device__ __forceinline__ void ld_early(const float* p, float& a, float& b, float& c, float& d) {
-    asm volatile("ld.global.cs.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(a), "=f"(b), "=f"(c), "=f"(d) : "l"(p));
+__device__ __forceinline__ float4 ld_early(const float* p) {
+    float4 v;
+    asm volatile("ld.global.cs.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+    return v;
 }
-__device__ __forceinline__ void ld_early(const float* p, const float* q, float2& a, float2& b) {
-    asm volatile("ld.global.cs.v2.f32 {%0, %1}, [%2];" : "=f"(a.x), "=f"(a.y) : "l"(p));
-    asm volatile("ld.global.cs.v2.f32 {%0, %1}, [%2];" : "=f"(b.x), "=f"(b.y) : "l"(q));
-}
-
-// A turned block to rows of `ld` elements: `rows` of its 32 rows, `cols` of its
-// 32 columns; out is at its first row and column. vec: pairs are aligned.
-template <typename T>
-__device__ __forceinline__ void turn_store(const float2* buf, T* out, int64_t ld, int rows, int cols, bool vec, int lane) {
-    const int p = lane & 15, hr = lane >> 4;
-    if (2 * p < cols) {
-        const bool two = 2 * p + 1 < cols;
-        T* o = out + hr * ld + 2 * p;
-#pragma unroll
-        for (int i0 = 0; i0 < 16; i0 += 8) {
-            float2 v[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = turn_get(buf, 2 * (i0 + i) + hr, p);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (2 * (i0 + i) + hr < rows) store_pair(o, v[i], two, vec);
-                o += 2 * ld;
-            }
-        }
-    }
-}
-
 template <bool MX4, bool AMN, bool BMN, int EPI>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
     dense_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
@@ -182,6 +188,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
         }
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (tid == 64) {
+        prefetch_map(&amap);
+        prefetch_map(&bmap);
+        if (MX4) {
+            prefetch_map(&samap);
+            prefetch_map(&sbmap);
+        }
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
@@ -283,7 +297,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
     } else if (warp >= kPEpi0) {
         // ------------------------------------------------------- epilogue
         const int qd = warp & 3, half = (warp - kPEpi0) >> 2;
-        float2* turn = reinterpret_cast<float2*>(smem + C::kTurnOff + (warp - kPEpi0) * 4096);
+        uint4* turn = reinterpret_cast<uint4*>(smem + C::kTurnOff + (warp - kPEpi0) * 4096);
         int acc = 0;
         uint32_t cph = 0;
         for (int t = blockIdx.x / 2; t < total; t += step) {
@@ -296,22 +310,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
             const int rows = int(max(int64_t(0), min(int64_t(32), a.M - m0)));
             if (EPI == kEpiStore) {
                 const int64_t end = min(a.N, int64_t(tn + 1) * BN);
-                for (int c = half * 32; c < BN; c += 64) {
-                    const int64_t n = int64_t(tn) * BN + c;
-                    if (n >= end) break;  // uniform over the warp
-                    const int cols = int(min(int64_t(32), end - n));
-                    float v[32];
-                    tmem_f32(tb + uint32_t(c), BN - c, v);
+                // 32 columns with the bias of theirs
+                auto fetch = [&](int c, int64_t n, float (&v)[32]) {
+                    tmem_f32(tb + uint32_t(c), v);
                     if (a.bias) {
-                        const float b = lane >= cols ? 0.0f
-                                        : a.out_f32  ? ((const float*)a.bias)[n + lane]
-                                                     : __bfloat162float(((const __nv_bfloat16*)a.bias)[n + lane]);
+                        const float b = n + lane >= end ? 0.0f
+                                        : a.out_f32     ? ((const float*)a.bias)[n + lane]
+                                                        : __bfloat162float(((const __nv_bfloat16*)a.bias)[n + lane]);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xffffffffu, b, i);
                     }
-                    turn_put(turn, lane, v);
-                    if (a.out_f32) turn_store(turn, (float*)a.out + m0 * a.N + n, a.N, rows, cols, a.vec_out, lane);
-                    else turn_store(turn, (__nv_bfloat16*)a.out + m0 * a.N + n, a.N, rows, cols, a.vec_out, lane);
+                };
+                float v[32];
+                if (a.out_f32) {
+                    for (int c = half * 32; c < BN; c += 64) {
+                        const int64_t n = int64_t(tn) * BN + c;
+                        if (n >= end) break;  // uniform over the warp
+                        fetch(c, n, v);
+                        put_f32(turn, lane, v);
+                        turn_out<8>(turn, (float*)a.out + m0 * a.N + n, a.N, rows, int(min(int64_t(32), end - n)), a.vec_out,
+                                    lane);
+                    }
+                } else {
+                    for (int c = half * 64; c < BN; c += 128) {
+                        const int64_t n = int64_t(tn) * BN + c;
+                        if (n >= end) break;
+                        uint4 w[8];
+                        fetch(c, n, v);
+                        pack32(v, w);
+                        if (n + 32 < end) {
+                            fetch(c + 32, n + 32, v);
+                            pack32(v, w + 4);
+                        }
+                        turn_put<8>(turn, lane, w);
+                        turn_out<8>(turn, (__nv_bfloat16*)a.out + m0 * a.N + n, a.N, rows, int(min(int64_t(64), end - n)),
+                                    a.vec_out, lane);
+                    }
                 }
             } else if (EPI == kEpiGate) {
                 const int bh = BN / 2;
@@ -320,8 +354,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
                     if (n >= a.N) break;
                     const int cols = int(min(int64_t(min(32, bh - c)), a.N - n));  // a multiple of 8, as N and bh are
                     float g[32], u[32];
-                    tmem_f32(tb + uint32_t(c), bh - c, g);
-                    tmem_f32(tb + uint32_t(bh + c), bh - c, u);
+                    tmem_f32(tb + uint32_t(c), g);
+                    tmem_f32(tb + uint32_t(bh + c), u);
                     if (a.bias) {
                         const __nv_bfloat16* b = (const __nv_bfloat16*)a.bias;
                         float bg = 0.0f, bu = 0.0f;
@@ -346,62 +380,84 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
                                     w[2 * i] = g[k + i];
                                     w[2 * i + 1] = u[k + i];
                                 }
-                                turn_put(turn, lane, w);
-                                turn_store(turn, gr + 2 * (n + k), 2 * a.N, rows, 2 * (cols - k), true, lane);
+                                put_f32(turn, lane, w);
+                                turn_out<8>(turn, gr + 2 * (n + k), 2 * a.N, rows, 2 * (cols - k), true, lane);
                             }
                         } else {
-                            turn_put(turn, lane, g);
-                            turn_store(turn, gr + n, 2 * a.N, rows, cols, true, lane);
-                            turn_put(turn, lane, u);
-                            turn_store(turn, gr + a.N + n, 2 * a.N, rows, cols, true, lane);
+                            put_f32(turn, lane, g);
+                            turn_out<8>(turn, gr + n, 2 * a.N, rows, cols, true, lane);
+                            put_f32(turn, lane, u);
+                            turn_out<8>(turn, gr + a.N + n, 2 * a.N, rows, cols, true, lane);
                         }
                     }
 #pragma unroll
                     for (int i = 0; i < 32; ++i) g[i] = gate_value(a.gate, g[i], u[i]);
-                    turn_put(turn, lane, g);
-                    turn_store(turn, (__nv_bfloat16*)a.out + m0 * a.N + n, a.N, rows, cols, true, lane);
+                    uint4 w[4];
+                    pack32(g, w);
+                    turn_put<4>(turn, lane, w);
+                    turn_out<4>(turn, (__nv_bfloat16*)a.out + m0 * a.N + n, a.N, rows, cols, true, lane);
                 }
             } else {
-                const int p = lane & 15, hr = lane >> 4;
+                // dh turned to eight lanes a row, four columns each, beside g and u
+                const int j = lane & 7, r0 = lane >> 3;
                 const int64_t end = min(a.N, int64_t(tn + 1) * BN);
                 for (int c = half * 32; c < BN; c += 64) {
                     const int64_t n = int64_t(tn) * BN + c;
                     if (n >= end) break;
                     float v[32];
-                    tmem_f32(tb + uint32_t(c), BN - c, v);
-                    turn_put(turn, lane, v);
-                    const int64_t col = n + 2 * p;
-                    // interleaved: (g, u, g, u) of the pair; else g and u pairs N apart
-                    const float* gr = a.gu + (m0 + hr) * 2 * a.N + (a.interleaved ? 2 * col : col);
-                    __nv_bfloat16* dr = (__nv_bfloat16*)a.dgu + (m0 + hr) * 2 * a.N + (a.interleaved ? 2 * col : col);
-                    __nv_bfloat16* hp = (__nv_bfloat16*)a.out + (m0 + hr) * a.N + col;
-                    const int mine = col < end ? rows - hr : 0;  // N is even: whole pairs
-                    if (mine > 0)
-                    for (int i0 = 0; i0 < 16; i0 += 8) {
-                        float2 g[8], u[8];
+                    tmem_f32(tb + uint32_t(c), v);
+                    put_f32(turn, lane, v);
+                    const int64_t col = n + 4 * j;
+                    const int mine = col < end ? rows - r0 : 0;  // N is a multiple of 8: whole fours
+                    if (mine > 0) {
+                        // interleaved: g, u, g, u, ...; else fours of g and of u, N apart
+                        const int64_t at = (m0 + r0) * 2 * a.N + (a.interleaved ? 2 * col : col);
+                        const int64_t apart = a.interleaved ? 4 : a.N;
+                        const float* gr = a.gu + at;
+                        __nv_bfloat16* dr = (__nv_bfloat16*)a.dgu + at;
+                        __nv_bfloat16* hp = (__nv_bfloat16*)a.out + (m0 + r0) * a.N + col;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            // a row past the end reads the last one: no branch keeps a load back
-                            const float* r = gr + int64_t(min(2 * (i0 + i), (mine - 1) & ~1)) * 2 * a.N;
-                            if (a.interleaved) ld_early(r, g[i].x, u[i].x, g[i].y, u[i].y);
-                            else ld_early(r, r + a.N, g[i], u[i]);
-                        }
+                        for (int i0 = 0; i0 < 8; i0 += 4) {
+                            float4 x[4], y[4];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int row = 2 * (i0 + i) + hr;
-                            if (row - hr >= mine) break;
-                            const float2 dh = turn_get(turn, row, p);
-                            float gx, ux, gy, uy;
-                            const float hx = gate_slopes(a.gate, g[i].x, u[i].x, gx, ux);
-                            const float hy = gate_slopes(a.gate, g[i].y, u[i].y, gy, uy);
-                            *reinterpret_cast<uint32_t*>(hp + int64_t(i0 + i) * 2 * a.N) = pack_bf16(hx, hy);
-                            __nv_bfloat16* d = dr + int64_t(i0 + i) * 4 * a.N;
-                            if (a.interleaved) {
-                                *reinterpret_cast<uint2*>(d) =
-                                    make_uint2(pack_bf16(dh.x * gx, dh.x * ux), pack_bf16(dh.y * gy, dh.y * uy));
-                            } else {
-                                *reinterpret_cast<uint32_t*>(d) = pack_bf16(dh.x * gx, dh.y * gy);
-                                *reinterpret_cast<uint32_t*>(d + a.N) = pack_bf16(dh.x * ux, dh.y * uy);
+                            for (int i = 0; i < 4; ++i) {
+                                // a row past the end reads the last one: no branch keeps a load back
+                                const float* r = gr + int64_t(min(4 * (i0 + i), (mine - 1) & ~3)) * 2 * a.N;
+                                x[i] = ld_early(r);
+                                y[i] = ld_early(r + apart);
+                            }
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int row = 4 * (i0 + i);  // after r0
+                                const uint4 q = turn[turn_at<8>(row + r0, j)];
+                                const float dh[4] = {__uint_as_float(q.x), __uint_as_float(q.y), __uint_as_float(q.z),
+                                                     __uint_as_float(q.w)};
+                                const float g[4] = {x[i].x, a.interleaved ? x[i].z : x[i].y, a.interleaved ? y[i].x : x[i].z,
+                                                    a.interleaved ? y[i].z : x[i].w};
+                                const float u[4] = {a.interleaved ? x[i].y : y[i].x, a.interleaved ? x[i].w : y[i].y,
+                                                    a.interleaved ? y[i].y : y[i].z, y[i].w};
+                                float h[4], dg[4], du[4];
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    float hg, hu;
+                                    h[k] = gate_slopes(a.gate, g[k], u[k], hg, hu);
+                                    dg[k] = dh[k] * hg;
+                                    du[k] = dh[k] * hu;
+                                }
+                                if (row < mine) {
+                                    *reinterpret_cast<uint2*>(hp + int64_t(row) * a.N) =
+                                        make_uint2(pack_bf16(h[0], h[1]), pack_bf16(h[2], h[3]));
+                                    __nv_bfloat16* d = dr + int64_t(row) * 2 * a.N;
+                                    if (a.interleaved) {
+                                        *reinterpret_cast<uint4*>(d) =
+                                            make_uint4(pack_bf16(dg[0], du[0]), pack_bf16(dg[1], du[1]),
+                                                       pack_bf16(dg[2], du[2]), pack_bf16(dg[3], du[3]));
+                                    } else {
+                                        *reinterpret_cast<uint2*>(d) = make_uint2(pack_bf16(dg[0], dg[1]), pack_bf16(dg[2], dg[3]));
+                                        *reinterpret_cast<uint2*>(d + a.N) =
+                                            make_uint2(pack_bf16(du[0], du[1]), pack_bf16(du[2], du[3]));
+                                    }
+                                }
                             }
                         }
                     }
@@ -499,7 +555,7 @@ cudaError_t launch_dense_pair(const DenseArgs& d, cudaStream_t st) {
     a.gate = d.gate;
     a.status = d.status;
     a.reset_status = d.reset_status;
-    a.vec_out = d.N % 2 == 0 && (reinterpret_cast<uintptr_t>(d.out) & (d.out_f32 ? 7 : 3)) == 0;
+    a.vec_out = d.N % (d.out_f32 ? 4 : 8) == 0 && (reinterpret_cast<uintptr_t>(d.out) & 15) == 0;
     CUtensorMap maps[4] = {};
     cudaError_t e;
     if (d.mx4) {

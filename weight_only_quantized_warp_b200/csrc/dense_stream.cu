@@ -125,6 +125,10 @@ __global__ void __launch_bounds__(kSThreads, 2)
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    if (tid == 64) {
+        prefetch_map(&wmap);
+        prefetch_map(&xmap);
+    }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                      "r"(C::kCols));

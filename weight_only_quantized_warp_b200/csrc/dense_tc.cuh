@@ -56,6 +56,10 @@ __device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity,
     return __all_sync(0xffffffffu, ok);
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
 // TMA load by one CTA of a pair, completing on a barrier that may be the
 // other CTA's (cluster address).
 __device__ __forceinline__ void tma_3d_pair_e(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar,
