@@ -173,13 +173,13 @@ struct DenseArgs {
 // scratch of dense_pair_workspace(M, N, K) bytes.
 void dense_pair_tiles(int64_t M, int64_t N, int64_t K, void* scratch, ScaleTiles* a, ScaleTiles* b);
 size_t dense_pair_workspace(int64_t M, int64_t N, int64_t K);
-cudaError_t launch_dense_pair(const DenseArgs& a, cudaStream_t st);
+// early: B was not written by the kernel before this one on the stream, so loads
+// of it need not wait for that kernel.
+cudaError_t launch_dense_pair(const DenseArgs& a, bool early, cudaStream_t st);
 
-// The same for few rows of A (along k): M up to kStreamRows. early_w: B was not
-// written by the kernel before this one on the stream, so loads of it need not
-// wait for that kernel.
+// The same for few rows of A (along k): M up to kStreamRows.
 constexpr int64_t kStreamRows = 64;
-cudaError_t launch_dense_stream(const DenseArgs& a, bool early_w, cudaStream_t st);
+cudaError_t launch_dense_stream(const DenseArgs& a, bool early, cudaStream_t st);
 
 // out[n] = sum_m x[m, n] (x [M, N] bf16) in a fixed order; part: workspace of
 // colsum_bytes(M, N).

@@ -126,8 +126,9 @@ struct FfnLayout : Layout {
 
 // Few rows stream the weights, more (and the weight gradients, whose rows are
 // weights) run on CTA pairs.
-cudaError_t launch_rows(const DenseArgs& a, bool early_w, cudaStream_t st) {
-    return a.M <= kStreamRows && (a.mx4 || a.a.k_step == 1) ? launch_dense_stream(a, early_w, st) : launch_dense_pair(a, st);
+cudaError_t launch_rows(const DenseArgs& a, bool early, cudaStream_t st) {
+    return a.M <= kStreamRows && (a.mx4 || a.a.k_step == 1) ? launch_dense_stream(a, early, st)
+                                                            : launch_dense_pair(a, early, st);
 }
 
 qmoe_status check_linear_sizes(int64_t T, int64_t N, int64_t K) {
@@ -364,7 +365,7 @@ qmoe_status qmoe_gated_ffn_backward(const qmoe_gated_ffn_config* cfg, int64_t T,
     void *h = ws + l.h, *dgu = ws + l.dgu;
     float* part = (float*)(ws + l.part);
     cudaError_t e = cudaSuccess;
-    auto product = [&](DenseOperand oa, DenseOperand ob, int64_t M, int64_t N, int64_t K, void* out) {
+    auto product = [&](DenseOperand oa, DenseOperand ob, int64_t M, int64_t N, int64_t K, void* out, bool early) {
         if (e != cudaSuccess || !out) return;
         DenseArgs a{};
         a.a = oa;
@@ -375,7 +376,7 @@ qmoe_status qmoe_gated_ffn_backward(const qmoe_gated_ffn_config* cfg, int64_t T,
         a.epi = kEpiStore;
         a.out = out;
         a.status = (int32_t*)workspace;
-        e = launch_rows(a, true, st);
+        e = launch_rows(a, early, st);
     };
     if (dx || dw1 || db1 || dw2) {
         DenseArgs a{};
@@ -396,9 +397,10 @@ qmoe_status qmoe_gated_ffn_backward(const qmoe_gated_ffn_config* cfg, int64_t T,
     } else if (e == cudaSuccess) {
         e = cudaMemsetAsync(workspace, 0, 4, st);
     }
-    product(cols_of(dy, H), cols_of(h, I), H, I, T, dw2);
-    product(rows_of(dgu, 2 * I), cols_of(w1, H), T, H, 2 * I, dx);
-    product(cols_of(dgu, 2 * I), cols_of(x, H), 2 * I, H, T, dw1);
+    // h and dgu come from the kernel before dx, not from the one before dw1 and dw2
+    product(rows_of(dgu, 2 * I), cols_of(w1, H), T, H, 2 * I, dx, true);
+    product(cols_of(dgu, 2 * I), cols_of(x, H), 2 * I, H, T, dw1, true);
+    product(cols_of(dy, H), cols_of(h, I), H, I, T, dw2, dx || dw1);
     if (e == cudaSuccess && db1) e = launch_colsum(dgu, T, 2 * I, db1, part, st);
     if (e == cudaSuccess && db2) e = launch_colsum(dy, T, H, db2, part, st);
     return e == cudaSuccess ? QMOE_OK : cuda_bad(e, "gated_ffn_backward");

@@ -49,6 +49,7 @@ struct PairArgs {
     GateParams gate;
     int32_t* status;
     int reset_status;
+    int early_b;           // B was not written by the kernel before this one
 };
 
 template <bool MX4>
@@ -206,8 +207,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
     cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    pdl_wait();  // everything up to here touched no global memory
-    pdl_trigger();
+    if (!(warp == 0 && a.early_b)) {  // everything up to here touched no global memory
+        pdl_wait();
+        pdl_trigger();
+    }
     if (a.reset_status && blockIdx.x == 0 && tid == 0) *a.status = 0;
     const int total = a.tiles_m * a.tiles_n, step = gridDim.x / 2;
 
@@ -219,35 +222,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
         bool ok = true;
         // bytes of both CTAs' copies of a stage
         const uint32_t bytes = 2u * uint32_t(kABytes + (BMN ? (BN > 128 ? 16384 : 8192) : BN * 64) + C::kSA + C::kSB);
+        auto load_b = [&](int tn, int ks, int s) {
+            const uint32_t sb = smem_u32(smem + s * C::kStage) + kABytes, fb = map_rank(smem_u32(&full[s]), 0);
+            const int n0 = EPI == kEpiGate ? tn * (BN / 2) : tn * BN + int(rank) * (BN / 2);
+            if (rank == 0) mbar_expect_tx_e(smem_u32(&full[s]), bytes, e);
+            if (BMN) {
+                tma_3d_pair_e(sb, &bmap, n0, ks * 64, 0, fb, e);
+                if (BN > 128) tma_3d_pair_e(sb + 8192, &bmap, n0 + 64, ks * 64, 0, fb, e);
+            } else {
+                tma_3d_pair_e(sb, &bmap, ks * (MX4 ? 128 : 64), n0, EPI == kEpiGate ? int(rank) : 0, fb, e);
+            }
+        };
+        auto load_a = [&](int tm, int tn, int ks, int s) {
+            const uint32_t sa = smem_u32(smem + s * C::kStage), fb = map_rank(smem_u32(&full[s]), 0);
+            const int m0 = tm * 256 + int(rank) * 128;
+            if (AMN) {
+                tma_3d_pair_e(sa, &amap, m0, ks * 64, 0, fb, e);
+                tma_3d_pair_e(sa + 8192, &amap, m0 + 64, ks * 64, 0, fb, e);
+            } else {
+                tma_3d_pair_e(sa, &amap, ks * (MX4 ? 128 : 64), m0, 0, fb, e);
+            }
+            if (MX4) {
+                const uint32_t ss = sa + kABytes + C::kB;
+                tma_3d_pair_e(ss, &samap, 0, (m0 >> 7) * (a.chunks >> 1) + ks, 0, fb, e);
+                tma_3d_pair_e(ss + C::kSA, &sbmap, 0, tn * a.chunks + 2 * ks, 0, fb, e);
+            }
+        };
+        int ks = 0;
+        if (a.early_b && int(blockIdx.x / 2) < total) {
+            // the first stages of B while the kernel before this one drains
+            int tm, tn;
+            pair_tile(a, blockIdx.x / 2, tm, tn);
+            const int first = min(ST, a.nks);
+            for (int i = 0; i < first; ++i) load_b(tn, i, i);
+            pdl_wait();
+            for (; ks < first; ++ks) load_a(tm, tn, ks, ks);
+            if (first == ST) ph = 1;
+            else st = first;
+        }
         for (int t = blockIdx.x / 2; ok && t < total; t += step) {
             int tm, tn;
             pair_tile(a, t, tm, tn);
-            const int m0 = tm * 256 + int(rank) * 128;
-            const int n0 = EPI == kEpiGate ? tn * (BN / 2) : tn * BN + int(rank) * (BN / 2);
-            const int zb = EPI == kEpiGate ? int(rank) : 0;
-            for (int ks = 0; ks < a.nks; ++ks) {
+            for (; ks < a.nks; ++ks) {
                 if (!warp_wait(smem_u32(&empty[st]), ph ^ 1u, abort_flag, a.status, kTimeoutNs)) { ok = false; break; }
-                const uint32_t sa = smem_u32(smem + st * C::kStage), sb = sa + kABytes;
-                const uint32_t fb = map_rank(smem_u32(&full[st]), 0);
-                if (rank == 0) mbar_expect_tx_e(smem_u32(&full[st]), bytes, e);
-                if (AMN) {
-                    tma_3d_pair_e(sa, &amap, m0, ks * 64, 0, fb, e);
-                    tma_3d_pair_e(sa + 8192, &amap, m0 + 64, ks * 64, 0, fb, e);
-                } else {
-                    tma_3d_pair_e(sa, &amap, ks * (MX4 ? 128 : 64), m0, 0, fb, e);
-                }
-                if (BMN) {
-                    tma_3d_pair_e(sb, &bmap, n0, ks * 64, 0, fb, e);
-                    if (BN > 128) tma_3d_pair_e(sb + 8192, &bmap, n0 + 64, ks * 64, 0, fb, e);
-                } else {
-                    tma_3d_pair_e(sb, &bmap, ks * (MX4 ? 128 : 64), n0, zb, fb, e);
-                }
-                if (MX4) {
-                    tma_3d_pair_e(sb + C::kB, &samap, 0, (m0 >> 7) * (a.chunks >> 1) + ks, 0, fb, e);
-                    tma_3d_pair_e(sb + C::kB + C::kSA, &sbmap, 0, tn * a.chunks + 2 * ks, 0, fb, e);
-                }
+                load_b(tn, ks, st);
+                load_a(tm, tn, ks, st);
                 if (++st == ST) { st = 0; ph ^= 1u; }
             }
+            ks = 0;
         }
     } else if (warp == 1 && rank == 0) {
         // ------------------------------------------------------- MMA issue
@@ -532,7 +554,7 @@ size_t dense_pair_workspace(int64_t M, int64_t N, int64_t K) {
     return size_t(up256(a.bytes()) + up256(b.bytes()));
 }
 
-cudaError_t launch_dense_pair(const DenseArgs& d, cudaStream_t st) {
+cudaError_t launch_dense_pair(const DenseArgs& d, bool early_b, cudaStream_t st) {
     const bool gate = d.epi == kEpiGate;
     PairArgs a{};
     a.M = d.M;
@@ -555,6 +577,7 @@ cudaError_t launch_dense_pair(const DenseArgs& d, cudaStream_t st) {
     a.gate = d.gate;
     a.status = d.status;
     a.reset_status = d.reset_status;
+    a.early_b = early_b;
     a.vec_out = d.N % (d.out_f32 ? 4 : 8) == 0 && (reinterpret_cast<uintptr_t>(d.out) & 15) == 0;
     CUtensorMap maps[4] = {};
     cudaError_t e;

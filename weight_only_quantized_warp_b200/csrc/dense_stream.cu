@@ -10,9 +10,12 @@
 // 128 W columns and the descriptor says MN-major.
 //
 // K is split over the CTAs of a cluster so that about two CTAs per SM stream
-// at once; their fp32 partials meet in shared memory and are added in rank
-// order through distributed shared memory (rank r finishes tokens r, r + S,
-// ...), so the result is the same on every call and there is no second launch.
+// at once. Rank r finishes tokens r, r + S, ...: every rank stores its fp32
+// partials of them into r's shared memory (over the rings, once all have
+// drained) and r adds them in rank order, so the result is the same on every
+// call and there is no second launch. Stores, not loads of the other ranks'
+// partials: those took a distributed-shared-memory latency per batch, 3.5 us of
+// 8 at T = 64, N = K = 2048.
 //
 // MX4 scales are read where they lie: 128 threads (the later epilogue) take 32
 // scales of a W row and of an X row at a time, four stages' worth, and place
@@ -48,7 +51,7 @@ struct StreamCfg {
     static constexpr int kS = MX4 ? 2048 : 0;  // W and X scales, 2 x 512 each
     static constexpr int kStage = kSW * (GATE ? 2 : 1) + kX + kS;
     static constexpr int kStages = (GATE ? 102 : 106) * 1024 / kStage;
-    static constexpr int kPart = NT * 128 * 4 * (GATE ? 2 : 1);  // partials, over the ring once it has drained
+    static constexpr int kPart = (NT + 8) * 512 * (GATE ? 2 : 1);  // partials, over the drained ring
     static constexpr int kRing = kStages * kStage > kPart ? kStages * kStage : kPart;
     static constexpr int kSmem = kRing + 1024 + 1024;
     static constexpr int kAcc = NT * (GATE ? 2 : 1);
@@ -116,18 +119,39 @@ __global__ void __launch_bounds__(kSThreads, 2)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accf + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-    if (tid == 0) {
-        for (int s = 0; s < ST; ++s) {
-            mbar_init(smem_u32(&full[s]), MX4 ? 5 : 1);
-            mbar_init(smem_u32(&empty[s]), 1);
+    const int first = min(ST, ks1 - ks0);  // stages in flight from the start
+    auto load_w = [&](int ks, int s, uint32_t e) {
+        const uint32_t sw = smem_u32(smem + s * C::kStage), fb = smem_u32(&full[s]);
+        mbar_expect_tx_e(fb, C::kStage - C::kS, e);
+        if (WMN) {
+            tma_3d_e(sw, &wmap, n0, ks * 64, 0, fb, e);
+            tma_3d_e(sw + 8192, &wmap, n0 + 64, ks * 64, 0, fb, e);
+        } else {
+            tma_3d_e(sw, &wmap, ks * KE, n0, 0, fb, e);
         }
-        mbar_init(smem_u32(accf), 1);
-        *abort_flag = 0;
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
-    if (tid == 64) {
-        prefetch_map(&wmap);
-        prefetch_map(&xmap);
+        if (GATE) tma_3d_e(sw + kSW, &wmap, ks * KE, n0, 1, fb, e);
+    };
+    auto load_x = [&](int ks, int s, uint32_t e) {
+        tma_3d_e(smem_u32(smem + s * C::kStage) + kSW * (GATE ? 2 : 1), &xmap, ks * KE, 0, 0, smem_u32(&full[s]), e);
+    };
+    if (warp == 0) {
+        if (lane == 0) {
+            for (int s = 0; s < ST; ++s) {
+                mbar_init(smem_u32(&full[s]), MX4 ? 5 : 1);
+                mbar_init(smem_u32(&empty[s]), 1);
+            }
+            mbar_init(smem_u32(accf), 1);
+            *abort_flag = 0;
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        }
+        __syncwarp();
+        // the first loads go out while the other warps set up; where W does not
+        // depend on the kernel before this one, also while that one drains
+        const uint32_t e = elect_one();
+        if (!a.early_w) pdl_wait();
+        for (int i = 0; i < first; ++i) load_w(ks0 + i, i, e);
+        if (a.early_w) pdl_wait();
+        for (int i = 0; i < first; ++i) load_x(ks0 + i, i, e);
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
@@ -138,12 +162,10 @@ __global__ void __launch_bounds__(kSThreads, 2)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    if (!(warp == 0 && a.early_w)) {  // everything up to here touched no global memory
-        pdl_wait();
-        // not before the wait: the next kernel's early loads count on all that
-        // came before this one being complete
-        pdl_trigger();
-    }
+    pdl_wait();
+    // not before the wait: the next kernel's early loads count on all that came
+    // before this one being complete
+    pdl_trigger();
     if (a.reset_status && blockIdx.x == 0 && tid == 32) *a.status = 0;
 
     if (warp == 0) {
@@ -151,30 +173,10 @@ __global__ void __launch_bounds__(kSThreads, 2)
         const uint32_t e = elect_one();
         int st = 0;
         uint32_t ph = 0;
-        const int first = min(ST, ks1 - ks0);
-        auto load_w = [&](int ks, int s) {
-            const uint32_t sw = smem_u32(smem + s * C::kStage), fb = smem_u32(&full[s]);
-            mbar_expect_tx_e(fb, C::kStage - C::kS, e);
-            if (WMN) {
-                tma_3d_e(sw, &wmap, n0, ks * 64, 0, fb, e);
-                tma_3d_e(sw + 8192, &wmap, n0 + 64, ks * 64, 0, fb, e);
-            } else {
-                tma_3d_e(sw, &wmap, ks * KE, n0, 0, fb, e);
-            }
-            if (GATE) tma_3d_e(sw + kSW, &wmap, ks * KE, n0, 1, fb, e);
-        };
-        auto load_x = [&](int ks, int s) {
-            tma_3d_e(smem_u32(smem + s * C::kStage) + kSW * (GATE ? 2 : 1), &xmap, ks * KE, 0, 0, smem_u32(&full[s]), e);
-        };
-        // where W does not depend on the kernel before this one, the ring fills
-        // with it while that kernel drains
-        for (int i = 0; i < first; ++i) load_w(ks0 + i, i);
-        if (a.early_w) pdl_wait();
-        for (int i = 0; i < first; ++i) load_x(ks0 + i, i);
         for (int ks = ks0 + first; ks < ks1; ++ks) {
             if (!warp_wait(smem_u32(&empty[st]), ph, abort_flag, a.status, kTimeoutNs)) break;
-            load_w(ks, st);
-            load_x(ks, st);
+            load_w(ks, st, e);
+            load_x(ks, st, e);
             if (++st == ST) { st = 0; ph ^= 1u; }
         }
     } else if (warp == 1) {
@@ -270,8 +272,17 @@ __global__ void __launch_bounds__(kSThreads, 2)
                                : __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(a.bias)[n]);
             }
         }
-        float* part = reinterpret_cast<float*>(smem);  // [accumulator][token][128]
+        // partials at their owner: [rank][token / splits][accumulator][128]
+        constexpr int NACC = GATE ? 2 : 1;
+        float* part = reinterpret_cast<float*>(smem);
+        const int per = (a.T + a.splits - 1) / a.splits;
+        if (a.splits > 1) {
+            __syncwarp();
+            cluster_sync_all();  // every ring has drained
+        }
         if (ok) {
+            const uint32_t mine = smem_u32(part) + uint32_t(rank * per * NACC * 512 + row * 4);
+            int owner = 0, slot = 0;
             for (int t0 = 0; t0 < a.T; t0 += 16) {
                 float v[16], u[16];
                 tmem_ld16(tb + uint32_t(t0), v);
@@ -285,8 +296,10 @@ __global__ void __launch_bounds__(kSThreads, 2)
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
                         if (t0 + j >= a.T) break;
-                        part[(t0 + j) * 128 + row] = v[j];
-                        if (GATE) part[(NT + t0 + j) * 128 + row] = u[j];
+                        const uint32_t to = map_rank(mine + uint32_t(slot * NACC * 512), uint32_t(owner));
+                        st_cluster_f32(to, v[j]);
+                        if (GATE) st_cluster_f32(to + 512, u[j]);
+                        if (++owner == a.splits) { owner = 0; ++slot; }
                     }
                 } else if (valid) {
                     stream_emit<EPI, 16>(a, t0, 1, a.T - t0, n, v, u, bg, bu);
@@ -295,20 +308,18 @@ __global__ void __launch_bounds__(kSThreads, 2)
             }
         }
         if (a.splits > 1) {
-            cluster_sync_all();
+            cluster_sync_all();  // every partial has arrived
             if (valid) {
                 constexpr int NB = 4;
-                const uint32_t base = smem_u32(part) + row * 4;
-                for (int t = rank; t < a.T; t += NB * a.splits) {
-                    const int left = (a.T - t + a.splits - 1) / a.splits;
+                for (int q = 0; rank + q * a.splits < a.T; q += NB) {
+                    const int t = rank + q * a.splits, left = (a.T - t + a.splits - 1) / a.splits;
                     float g[NB] = {}, u[NB] = {};
                     for (int s = 0; s < a.splits; ++s) {
-                        const uint32_t from = map_rank(base, uint32_t(s));
 #pragma unroll
                         for (int j = 0; j < NB; ++j) {
-                            const uint32_t at = uint32_t(t + min(j, left - 1) * a.splits);
-                            g[j] += ld_cluster_f32(from + at * 512);
-                            if (GATE) u[j] += ld_cluster_f32(from + (NT + at) * 512);
+                            const float* p = part + ((s * per + q + min(j, left - 1)) * NACC) * 128 + row;
+                            g[j] += p[0];
+                            if (GATE) u[j] += p[128];
                         }
                     }
                     stream_emit<EPI, NB>(a, t, a.splits, left, n, g, u, bg, bu);
@@ -316,14 +327,17 @@ __global__ void __launch_bounds__(kSThreads, 2)
             }
         }
     }
-    if (a.splits > 1 && warp < 2) cluster_sync_all();
+    if (a.splits > 1 && warp < 2) {
+        __syncwarp();
+        cluster_sync_all();
+        cluster_sync_all();
+    }
     __syncwarp();
     if (*abort_flag) {  // copies of the abandoned stages land before the memory goes away
         for (int i = 0; i < 1000; ++i) __nanosleep(1000);
     }
     tc_fence_before();
-    if (a.splits > 1) cluster_sync_all();  // nobody leaves while its partials are read
-    else __syncthreads();
+    __syncthreads();
     if (warp == 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols));

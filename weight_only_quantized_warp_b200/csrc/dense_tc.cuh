@@ -122,11 +122,9 @@ __device__ __forceinline__ void cp_scales_e(uint32_t t, uint64_t sdesc, uint32_t
         "l"(sdesc), "r"(e)
         : "memory");
 }
-// A float of another CTA's shared memory (cluster address).
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
+// A float to another CTA's shared memory (cluster address).
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
 // Shared-memory descriptor of an operand whose rows (M or N) lie along
