@@ -181,9 +181,14 @@ cudaError_t launch_dense_pair(const DenseArgs& a, bool early, cudaStream_t st);
 constexpr int64_t kStreamRows = 64;
 cudaError_t launch_dense_stream(const DenseArgs& a, bool early, cudaStream_t st);
 
-// out[n] = sum_m x[m, n] (x [M, N] bf16) in a fixed order; part: workspace of
-// colsum_bytes(M, N).
-size_t colsum_bytes(int64_t M, int64_t N);
-cudaError_t launch_colsum(const void* x, int64_t M, int64_t N, void* out, float* part, cudaStream_t st);
+// out[n] = sum_m x[m, n] (x [M, N] bf16, out bf16; skipped when out is null) in a
+// fixed order, for up to two matrices; part: workspace of colsum_bytes.
+struct ColSum {
+    const void* x;
+    int64_t N;
+    void* out;
+};
+size_t colsum_bytes(int64_t M, int64_t Na, int64_t Nb);
+cudaError_t launch_colsum(const ColSum& a, const ColSum& b, int64_t M, float* part, cudaStream_t st);
 
 }  // namespace qmoe

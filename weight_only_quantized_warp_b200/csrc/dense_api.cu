@@ -118,8 +118,7 @@ struct FfnLayout : Layout {
         h = take(size_t(T) * c.inter_size * 2);
         if (backward) {
             dgu = take(size_t(T) * c.inter_size * 4);
-            const size_t p1 = colsum_bytes(T, 2 * c.inter_size), p2 = colsum_bytes(T, c.hidden_size);
-            part = take(p1 > p2 ? p1 : p2);
+            part = take(colsum_bytes(T, 2 * c.inter_size, c.hidden_size));
         }
     }
 };
@@ -401,8 +400,7 @@ qmoe_status qmoe_gated_ffn_backward(const qmoe_gated_ffn_config* cfg, int64_t T,
     product(rows_of(dgu, 2 * I), cols_of(w1, H), T, H, 2 * I, dx, true);
     product(cols_of(dgu, 2 * I), cols_of(x, H), 2 * I, H, T, dw1, true);
     product(cols_of(dy, H), cols_of(h, I), H, I, T, dw2, dx || dw1);
-    if (e == cudaSuccess && db1) e = launch_colsum(dgu, T, 2 * I, db1, part, st);
-    if (e == cudaSuccess && db2) e = launch_colsum(dy, T, H, db2, part, st);
+    if (e == cudaSuccess) e = launch_colsum({dgu, 2 * I, db1}, {dy, H, db2}, T, part, st);
     return e == cudaSuccess ? QMOE_OK : cuda_bad(e, "gated_ffn_backward");
 }
 

@@ -1,8 +1,10 @@
-// dense_colsum.cu -- column sums of a bf16 matrix (the bias gradients),
-// sm_100a. HBM-bound: one read of the matrix. The rows are cut into S ranges;
-// a CTA sums 256 columns of one range (eight warps take alternate rows, a lane
-// 16 bytes, joined through shared memory in warp order) and a second kernel
-// adds the S partials in order, so the result does not depend on timing.
+// dense_colsum.cu -- column sums of one or two bf16 matrices of the same row
+// count (the bias gradients), sm_100a. HBM-bound: one read of the matrices. The
+// rows are cut into S ranges; a CTA sums 256 columns of one range (eight warps
+// take alternate rows, a lane 16 bytes, joined through shared memory in warp
+// order) and a second kernel adds the S partials in order, so the result does
+// not depend on timing. Both matrices share the launches: at T = 1023 and 5760 +
+// 2880 columns four launches took 22 us, two take 11.
 #include "dense.cuh"
 
 namespace qmoe {
@@ -10,20 +12,34 @@ namespace {
 
 constexpr int kColWarps = 8;
 
-__global__ void __launch_bounds__(kColWarps * 32) colsum_part_kernel(const __nv_bfloat16* x, int64_t M,
-                                                                    int64_t N, int64_t rows_per,
-                                                                    float* part) {
+// Columns of both matrices side by side, 256 a CTA: a's first.
+struct ColPair {
+    ColSum a, b;
+    int64_t M;
+    int blocks_a;
+};
+
+__device__ __forceinline__ const ColSum& col_block(const ColPair& p, int64_t& c0) {
+    const bool second = int(blockIdx.x) >= p.blocks_a;
+    c0 = int64_t(int(blockIdx.x) - (second ? p.blocks_a : 0)) * 256;
+    return second ? p.b : p.a;
+}
+
+__global__ void __launch_bounds__(kColWarps * 32) colsum_part_kernel(const ColPair p, int64_t rows_per, float* part) {
     __shared__ float sum[kColWarps][256];
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t c = int64_t(blockIdx.x) * 256 + lane * 8;  // N is a multiple of 8
-    const int64_t m0 = blockIdx.y * rows_per, m1 = min(M, m0 + rows_per);
+    int64_t c0;
+    const ColSum& s = col_block(p, c0);
+    const int64_t c = c0 + lane * 8;  // N is a multiple of 8
+    const int64_t m0 = blockIdx.y * rows_per, m1 = min(p.M, m0 + rows_per);
+    const __nv_bfloat16* x = reinterpret_cast<const __nv_bfloat16*>(s.x);
     float acc[8] = {};
-    if (c < N) {
+    if (c < s.N) {
 #pragma unroll 4
         for (int64_t m = m0 + warp; m < m1; m += kColWarps) {
-            const uint4 v = *reinterpret_cast<const uint4*>(x + m * N + c);
+            const uint4 v = *reinterpret_cast<const uint4*>(x + m * s.N + c);
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -35,44 +51,53 @@ __global__ void __launch_bounds__(kColWarps * 32) colsum_part_kernel(const __nv_
 #pragma unroll
     for (int i = 0; i < 8; ++i) sum[warp][lane * 8 + i] = acc[i];
     __syncthreads();
-    const int64_t n = int64_t(blockIdx.x) * 256 + threadIdx.x;
-    if (n < N) {
-        float s = 0.0f;
+    float t = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kColWarps; ++w) s += sum[w][threadIdx.x];
-        part[blockIdx.y * N + n] = s;
-    }
+    for (int w = 0; w < kColWarps; ++w) t += sum[w][threadIdx.x];
+    part[(int64_t(blockIdx.y) * gridDim.x + blockIdx.x) * 256 + threadIdx.x] = t;
 }
 
-__global__ void __launch_bounds__(256) colsum_join_kernel(const float* part, int64_t N, int splits,
-                                                          __nv_bfloat16* out) {
+__global__ void __launch_bounds__(256) colsum_join_kernel(const ColPair p, int splits, const float* part) {
     pdl_wait();
     pdl_trigger();
-    const int64_t n = int64_t(blockIdx.x) * 256 + threadIdx.x;
-    if (n >= N) return;
-    float s = 0.0f;
-    for (int i = 0; i < splits; ++i) s += part[i * N + n];
-    out[n] = __float2bfloat16_rn(s);
+    int64_t c0;
+    const ColSum& s = col_block(p, c0);
+    const int64_t c = c0 + threadIdx.x;
+    if (c >= s.N) return;
+    float t = 0.0f;
+#pragma unroll 8
+    for (int i = 0; i < splits; ++i) t += part[(int64_t(i) * gridDim.x + blockIdx.x) * 256 + threadIdx.x];
+    reinterpret_cast<__nv_bfloat16*>(s.out)[c] = __float2bfloat16_rn(t);
 }
 
-// Row ranges: about two CTAs per SM, at least 32 rows each.
-int64_t col_splits(int64_t M, int64_t N) {
-    const int64_t want = (2 * 148 * 256 + N - 1) / N, most = (M + 31) / 32;
+int64_t col_blocks(const ColSum& s) { return s.out ? (s.N + 255) / 256 : 0; }
+
+// Row ranges: about four CTAs per SM, at least 32 rows each.
+int64_t col_splits(int64_t M, int64_t blocks) {
+    const int64_t want = (4 * 148 + blocks - 1) / blocks, most = (M + 31) / 32;
     return want < 1 ? 1 : (want < most ? want : most);
 }
 
 }  // namespace
 
-size_t colsum_bytes(int64_t M, int64_t N) { return size_t(col_splits(M, N)) * size_t(N) * 4; }
+size_t colsum_bytes(int64_t M, int64_t Na, int64_t Nb) {
+    // whichever of the sums are asked for: fewer blocks take more ranges, up to
+    // one more CTA per block than with both
+    const int64_t blocks = (Na + 255) / 256 + (Nb + 255) / 256, ranges = (M + 31) / 32;
+    const int64_t ctas = blocks * (ranges < 1 ? 1 : ranges);
+    const int64_t cap = 4 * 148 + blocks;
+    return size_t(ctas < cap ? ctas : cap) * 1024;
+}
 
-cudaError_t launch_colsum(const void* x, int64_t M, int64_t N, void* out, float* part, cudaStream_t st) {
-    const int64_t s = col_splits(M, N), per = (M + s - 1) / s;
-    const unsigned nb = unsigned((N + 255) / 256);
-    cudaError_t e = launch_kernel(colsum_part_kernel, dim3(nb, unsigned(s)), dim3(kColWarps * 32), 0, st, true,
-                                  (const __nv_bfloat16*)x, M, N, per, part);
+cudaError_t launch_colsum(const ColSum& a, const ColSum& b, int64_t M, float* part, cudaStream_t st) {
+    const ColPair p{a, b, M, int(col_blocks(a))};
+    const int64_t blocks = col_blocks(a) + col_blocks(b);
+    if (blocks == 0) return cudaSuccess;
+    const int64_t s = col_splits(M, blocks), per = (M + s - 1) / s;
+    const cudaError_t e = launch_kernel(colsum_part_kernel, dim3(unsigned(blocks), unsigned(s)), dim3(kColWarps * 32), 0, st,
+                                        true, p, per, part);
     if (e != cudaSuccess) return e;
-    return launch_kernel(colsum_join_kernel, dim3(nb), dim3(256), 0, st, true, (const float*)part, N, int(s),
-                         (__nv_bfloat16*)out);
+    return launch_kernel(colsum_join_kernel, dim3(unsigned(blocks)), dim3(256), 0, st, true, p, int(s), (const float*)part);
 }
 
 }  // namespace qmoe

@@ -116,11 +116,12 @@ __device__ __forceinline__ void pack32(const float (&v)[32], uint4* w) {
 
 // A turned block to rows of `ld` elements: `rows` of its rows, `cols` of its
 // columns; out is at its first element. vec: rows start on 16 bytes.
-// Otherwise lanes take words of a row, as whole words where those are aligned.
+// Otherwise (eight units) lanes take words of a row, whole where those are
+// aligned.
 template <int NU, typename T>
 __device__ __forceinline__ void turn_out(const uint4* buf, T* out, int64_t ld, int rows, int cols, bool vec, int lane) {
     constexpr int E = 16 / int(sizeof(T)), RI = 32 / NU;
-    if (vec) {
+    if (NU != 8 || vec) {
         const int j = lane % NU, r0 = lane / NU;
         T* o = out + r0 * ld + j * E;
         const bool mine = j * E < cols;  // cols is a multiple of E where rows are aligned
@@ -134,20 +135,30 @@ __device__ __forceinline__ void turn_out(const uint4* buf, T* out, int64_t ld, i
         }
         return;
     }
-    const uint32_t* words = reinterpret_cast<const uint32_t*>(buf);
-    constexpr int EW = 4 / int(sizeof(T));  // elements of a word
-    const bool whole = EW == 1 || (((reinterpret_cast<uintptr_t>(out) & 3) == 0) && ld % 2 == 0);
-    for (int r = 0; r < rows; ++r)
-        for (int w = lane; w < NU * 4; w += 32) {
-            const uint32_t v = words[turn_at<NU>(r, w >> 2) * 4 + (w & 3)];
-            T* o = out + r * ld + w * EW;
-            if (w * EW + EW <= cols && whole) {
-                *reinterpret_cast<uint32_t*>(o) = v;
-            } else if (EW == 2) {
-                if (2 * w < cols) reinterpret_cast<uint16_t*>(o)[0] = uint16_t(v);
-                if (2 * w + 1 < cols) reinterpret_cast<uint16_t*>(o)[1] = uint16_t(v >> 16);
+    if constexpr (NU == 8) {  // a line is 32 words, one a lane
+        const uint32_t* words = reinterpret_cast<const uint32_t*>(buf);
+        constexpr int EW = 4 / int(sizeof(T));  // elements of a word
+        const bool whole = EW == 1 || (((reinterpret_cast<uintptr_t>(out) & 3) == 0) && ld % 2 == 0);
+        T* o = out + lane * EW;
+#pragma unroll
+        for (int r0 = 0; r0 < 32; r0 += 8) {
+            uint32_t v[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r) v[r] = words[turn_at<NU>(r0 + r, lane >> 2) * 4 + (lane & 3)];
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                if (r0 + r < rows) {
+                    if (lane * EW + EW <= cols && whole) {
+                        *reinterpret_cast<uint32_t*>(o) = v[r];
+                    } else if (EW == 2) {
+                        if (2 * lane < cols) reinterpret_cast<uint16_t*>(o)[0] = uint16_t(v[r]);
+                        if (2 * lane + 1 < cols) reinterpret_cast<uint16_t*>(o)[1] = uint16_t(v[r] >> 16);
+                    }
+                }
+                o += ld;
             }
         }
+    }
 }
 
 // Loads that stay where they are written, ahead of the arithmetic: a batch of
@@ -164,7 +175,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
                       const PairArgs a) {
     using C = PairCfg<MX4>;
     constexpr int ST = C::kStages;
-    const int BN = MX4 ? C::BN : a.bn;  // 240 is fixed by the scales' columns
+    const int BN = a.bn;  // up to C::BN
     extern __shared__ uint8_t smem_raw[];
     // the dynamic segment starts at the same address in both CTAs, so the
     // aligned offsets agree
@@ -221,7 +232,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
         uint32_t ph = 0;
         bool ok = true;
         // bytes of both CTAs' copies of a stage
-        const uint32_t bytes = 2u * uint32_t(kABytes + (BMN ? (BN > 128 ? 16384 : 8192) : BN * 64) + C::kSA + C::kSB);
+        const uint32_t bytes = 2u * uint32_t(kABytes + (BMN ? (BN > 128 ? 16384 : 8192) : BN * 64) +
+                                             (MX4 ? C::kSA + (BN > 128 ? C::kSB : C::kSB / 2) : 0));
         auto load_b = [&](int tn, int ks, int s) {
             const uint32_t sb = smem_u32(smem + s * C::kStage) + kABytes, fb = map_rank(smem_u32(&full[s]), 0);
             const int n0 = EPI == kEpiGate ? tn * (BN / 2) : tn * BN + int(rank) * (BN / 2);
@@ -244,8 +256,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
             }
             if (MX4) {
                 const uint32_t ss = sa + kABytes + C::kB;
-                tma_3d_pair_e(ss, &samap, 0, (m0 >> 7) * (a.chunks >> 1) + ks, 0, fb, e);
-                tma_3d_pair_e(ss + C::kSA, &sbmap, 0, tn * a.chunks + 2 * ks, 0, fb, e);
+                tma_3d_pair_e(ss, &samap, 0, (m0 >> 7) * a.chunks + 2 * ks, 0, fb, e);
+                // rows of 512 bytes: a chunk of up to 128 tile rows
+                tma_3d_pair_e(ss + C::kSA, &sbmap, 0, (tn * a.chunks + 2 * ks) * (BN > 128 ? 2 : 1), 0, fb, e);
             }
         };
         int ks = 0;
@@ -293,13 +306,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         cp_scales_pair_e(tscale + 4 * j, desc_scales(ssa + 512 * j), e);
-                        cp_scales_pair_e(tscale + 8 + 8 * j, desc_scales(ssb + 1024 * j), e);
-                        cp_scales_pair_e(tscale + 12 + 8 * j, desc_scales(ssb + 1024 * j + 512), e);
+                        cp_scales_pair_e(tscale + 8 + 8 * j, desc_scales(ssb + (BN > 128 ? 1024 : 512) * j), e);
+                        if (BN > 128) cp_scales_pair_e(tscale + 12 + 8 * j, desc_scales(ssb + 1024 * j + 512), e);
                     }
                     const uint64_t ad = desc_sw128(sa), bd = desc_sw128(sb);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        mma_mx4_pair_e(d, ad + uint64_t(2 * kk), bd + uint64_t(2 * kk), idesc_mx4(256, C::BN, 2 * (kk & 1)),
+                        mma_mx4_pair_e(d, ad + uint64_t(2 * kk), bd + uint64_t(2 * kk), idesc_mx4(256, BN, 2 * (kk & 1)),
                                        tscale + 4 * (kk >> 1), tscale + 8 + 8 * (kk >> 1), kk > 0 ? 1u : acc0, e);
                 } else {
                     const uint64_t ad = AMN ? desc_mn128(sa) : desc_sw128(sa);
@@ -516,19 +529,20 @@ cudaError_t launch_one(const CUtensorMap (&maps)[4], const PairArgs& a, cudaStre
                          maps[2], maps[3], a);
 }
 
-// Tile columns of a bf16 product: 256 where the tiles fill many rounds of the
-// pairs. With few rounds a narrower tile can save a large part of the last,
-// half-empty one: the width (a multiple of 32, at least 128) with the smallest
-// rounds x (BN + 256), a stage's operand bytes per CTA, which is what a stage
-// takes below 256 columns. Measured at T = 1024, H = I = 2880 (160 columns)
-// against 256 throughout: forward 56.7 against 67.6 us, training step 194
-// against 217 us; 160 columns at T = 4096, H = 4096, I = 14336 (where the rule
-// keeps 256) take 3792 us against 3120.
-int pair_width(int64_t tiles_m, int64_t n, int pairs) {
-    int best = 256;
+// Tile columns: the widest (256; 240 for MX4) where the tiles fill many rounds
+// of the 74 pairs. With few rounds a narrower tile can save a large part of the
+// last, half-empty one: the width (a multiple of 32, at least 128) with the
+// smallest rounds x (BN + 256), a stage's operand bytes per CTA, which is what a
+// stage takes below 256 columns. Measured at T = 1024, H = I = 2880 (160
+// columns) against 256 throughout: forward 56.7 against 67.6 us, training step
+// 194 against 217 us; 160 columns at T = 4096, H = 4096, I = 14336 (where the
+// rule keeps 256) take 3792 us against 3120.
+int pair_width(int64_t tiles_m, int64_t n, bool mx4) {
+    constexpr int64_t kPairs = 74;
+    int best = 0;
     int64_t cost = INT64_MAX;
-    for (int bn = 256; bn >= 128; bn -= 32) {
-        const int64_t tiles = tiles_m * ((n + bn - 1) / bn), c = (tiles + pairs - 1) / pairs * (bn + 256);
+    for (int bn = mx4 ? PairCfg<true>::BN : 256; bn >= 128; bn = (bn - 1) / 32 * 32) {
+        const int64_t tiles = tiles_m * ((n + bn - 1) / bn), c = (tiles + kPairs - 1) / kPairs * (bn + 256);
         if (c < cost) {
             cost = c;
             best = bn;
@@ -543,7 +557,7 @@ int64_t up256(int64_t v) { return (v + 255) & ~int64_t(255); }
 }  // namespace
 
 void dense_pair_tiles(int64_t M, int64_t N, int64_t K, void* scratch, ScaleTiles* a, ScaleTiles* b) {
-    const int BN = PairCfg<true>::BN;
+    const int BN = pair_width((M + 255) / 256, N, true);
     *a = {nullptr, (uint8_t*)scratch, M, 128, int((M + 255) / 256) * 2, int(pair_chunks(K))};
     *b = {nullptr, (uint8_t*)scratch + up256(a->bytes()), N, BN, int((N + BN - 1) / BN), a->chunks};
 }
@@ -561,7 +575,7 @@ cudaError_t launch_dense_pair(const DenseArgs& d, bool early_b, cudaStream_t st)
     a.N = gate ? d.N / 2 : d.N;
     a.K = d.K;
     a.tiles_m = int((d.M + 255) / 256);
-    const int BN = d.mx4 ? 240 : pair_width(a.tiles_m, d.N, sm_count() / 2);
+    const int BN = pair_width(a.tiles_m, d.N, d.mx4 != 0);
     a.bn = BN;
     const int64_t tn = (a.N + (gate ? BN / 2 : BN) - 1) / (gate ? BN / 2 : BN);
     if (int64_t(a.tiles_m) * tn > (int64_t(1) << 30)) return cudaErrorInvalidValue;
@@ -592,12 +606,12 @@ cudaError_t launch_dense_pair(const DenseArgs& d, bool early_b, cudaStream_t st)
             MapSpec sc{};
             sc.p = t[i].out;
             sc.type = CU_TENSOR_MAP_DATA_TYPE_INT32;
-            sc.dims[0] = 256;
-            sc.dims[1] = uint64_t(t[i].bytes() / 1024);
+            sc.dims[0] = 128;
+            sc.dims[1] = uint64_t(t[i].bytes() / 512);
             sc.dims[2] = 1;
-            sc.strides[0] = sc.strides[1] = 1024;
-            sc.box[0] = 256;
-            sc.box[1] = i ? 2 : 1;
+            sc.strides[0] = sc.strides[1] = 512;
+            sc.box[0] = 128;
+            sc.box[1] = uint32_t(2 * t[i].subs());  // a stage's two chunks
             sc.box[2] = 1;
             if ((e = encode_map(&maps[2 + i], sc)) != cudaSuccess) return e;
         }
