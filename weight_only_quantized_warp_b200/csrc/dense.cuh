@@ -177,6 +177,13 @@ size_t dense_pair_workspace(int64_t M, int64_t N, int64_t K);
 // of it need not wait for that kernel.
 cudaError_t launch_dense_pair(const DenseArgs& a, bool early, cudaStream_t st);
 
+// Up to three plain products (kEpiStore, bf16, B across its rows) in one launch,
+// any of them null: a long one, and two of the same K that fill in around it.
+// B of the first two was not written by the kernel before this one; early3 says
+// so of the third.
+cudaError_t launch_dense_pairs(const DenseArgs* first, const DenseArgs* second, const DenseArgs* third, bool early3,
+                               cudaStream_t st);
+
 // The same for few rows of A (along k): M up to kStreamRows.
 constexpr int64_t kStreamRows = 64;
 cudaError_t launch_dense_stream(const DenseArgs& a, bool early, cudaStream_t st);

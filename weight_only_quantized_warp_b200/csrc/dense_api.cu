@@ -123,11 +123,9 @@ struct FfnLayout : Layout {
     }
 };
 
-// Few rows stream the weights, more (and the weight gradients, whose rows are
-// weights) run on CTA pairs.
+// Few rows stream the weights, more run on CTA pairs.
 cudaError_t launch_rows(const DenseArgs& a, bool early, cudaStream_t st) {
-    return a.M <= kStreamRows && (a.mx4 || a.a.k_step == 1) ? launch_dense_stream(a, early, st)
-                                                            : launch_dense_pair(a, early, st);
+    return a.M <= kStreamRows ? launch_dense_stream(a, early, st) : launch_dense_pair(a, early, st);
 }
 
 qmoe_status check_linear_sizes(int64_t T, int64_t N, int64_t K) {
@@ -364,8 +362,7 @@ qmoe_status qmoe_gated_ffn_backward(const qmoe_gated_ffn_config* cfg, int64_t T,
     void *h = ws + l.h, *dgu = ws + l.dgu;
     float* part = (float*)(ws + l.part);
     cudaError_t e = cudaSuccess;
-    auto product = [&](DenseOperand oa, DenseOperand ob, int64_t M, int64_t N, int64_t K, void* out, bool early) {
-        if (e != cudaSuccess || !out) return;
+    auto product = [&](DenseOperand oa, DenseOperand ob, int64_t M, int64_t N, int64_t K, void* out) {
         DenseArgs a{};
         a.a = oa;
         a.b = ob;
@@ -375,7 +372,7 @@ qmoe_status qmoe_gated_ffn_backward(const qmoe_gated_ffn_config* cfg, int64_t T,
         a.epi = kEpiStore;
         a.out = out;
         a.status = (int32_t*)workspace;
-        e = launch_rows(a, early, st);
+        return a;
     };
     if (dx || dw1 || db1 || dw2) {
         DenseArgs a{};
@@ -396,10 +393,14 @@ qmoe_status qmoe_gated_ffn_backward(const qmoe_gated_ffn_config* cfg, int64_t T,
     } else if (e == cudaSuccess) {
         e = cudaMemsetAsync(workspace, 0, 4, st);
     }
-    // h and dgu come from the kernel before dx, not from the one before dw1 and dw2
-    product(rows_of(dgu, 2 * I), cols_of(w1, H), T, H, 2 * I, dx, true);
-    product(cols_of(dgu, 2 * I), cols_of(x, H), 2 * I, H, T, dw1, true);
-    product(cols_of(dy, H), cols_of(h, I), H, I, T, dw2, dx || dw1);
+    const DenseArgs pdx = product(rows_of(dgu, 2 * I), cols_of(w1, H), T, H, 2 * I, dx);
+    const DenseArgs pw1 = product(cols_of(dgu, 2 * I), cols_of(x, H), 2 * I, H, T, dw1);
+    const DenseArgs pw2 = product(cols_of(dy, H), cols_of(h, I), H, I, T, dw2);
+    const bool stream_dx = dx && T <= kStreamRows;
+    if (e == cudaSuccess && stream_dx) e = launch_dense_stream(pdx, true, st);
+    // h comes from the kernel before dx: known to be complete after dx's launch only
+    if (e == cudaSuccess && ((dx && !stream_dx) || dw1 || dw2))
+        e = launch_dense_pairs(dx && !stream_dx ? &pdx : nullptr, dw1 ? &pw1 : nullptr, dw2 ? &pw2 : nullptr, stream_dx, st);
     if (e == cudaSuccess) e = launch_colsum({dgu, 2 * I, db1}, {dy, H, db2}, T, part, st);
     return e == cudaSuccess ? QMOE_OK : cuda_bad(e, "gated_ffn_backward");
 }

@@ -37,19 +37,35 @@ constexpr int kPEpi0 = 4, kPEpiWarps = 8;
 constexpr int kGroupM = 8;  // 2, 4 and 16 measured the same
 constexpr int kABytes = 128 * 128;  // one CTA's A rows of a stage
 
-struct PairArgs {
-    int64_t M, N, K;       // N: result columns (h columns for the gate)
-    int tiles_m, tiles_n, nks, chunks;
+// One product of a launch.
+struct PairProblem {
+    int64_t M, N;          // N: result columns (h columns for the gate)
+    int tiles_m, tiles_n, nks;
     int bn;                // columns of a tile (accumulators, both halves)
-    int epi, out_f32, interleaved, vec_out;
-    const void* bias;
+    int amn;               // A lies MN-major (launches of several products)
+    int early_b;           // B was not written by the kernel before this one
+    int vec_out;
     void* out;
+};
+
+// A launch walks up to three products: the tiles of p[0], then those of p[1] and
+// p[2] as one list (the backward pass's dx, and dw1 and dw2, which are shorter).
+struct PairArgs {
+    PairProblem p[3];
+    int tiles[3];
+    int head;              // see tile_at
+    int chunks;
+    int out_f32, interleaved;
+    const void* bias;
     float* gu;
     void* dgu;
     GateParams gate;
     int32_t* status;
     int reset_status;
-    int early_b;           // B was not written by the kernel before this one
+};
+
+struct PairMaps {
+    CUtensorMap a[3], b[3];  // MX4: a[1], b[1] are the tiled scales
 };
 
 template <bool MX4>
@@ -65,11 +81,31 @@ struct PairCfg {
     static_assert(kStage % 1024 == 0 && kSmem <= 227 * 1024, "stages");
 };
 
-__device__ __forceinline__ void pair_tile(const PairArgs& a, int t, int& tm, int& tn) {
-    const int per = kGroupM * a.tiles_n;
-    const int g = t / per, m0 = g * kGroupM, gm = min(a.tiles_m - m0, kGroupM), r = t - g * per;
-    tm = m0 + r % gm;
-    tn = r / gm;
+// The i-th tile of a pair. p[0]'s tiles go round the pairs. Where they do not
+// come out even, the pairs left with one fewer start on the second list `head`
+// of its tiles early (as many as take the time of one of p[0]'s), and the rest
+// of that list goes round all pairs.
+template <bool MULTI>
+__device__ __forceinline__ bool tile_at(const PairArgs& a, int i, int& q, int& tm, int& tn) {
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1, D = a.tiles[0], W = a.tiles[1] + a.tiles[2];
+    int t = pair + i * pairs;
+    q = 0;
+    if (t >= D) {
+        if (!MULTI || W == 0) return false;
+        const int r = D % pairs, E = r ? pairs - r : 0, base = min(W, E * a.head);
+        i -= pair < D ? (D - 1 - pair) / pairs + 1 : 0;
+        t = base + pair + i * pairs;
+        if (E && pair >= r) t = i < a.head ? pair - r + i * E : t - a.head * pairs;
+        if (t >= (E && pair >= r && i < a.head ? base : W)) return false;
+        q = t < a.tiles[1] ? 1 : 2;
+        if (q == 2) t -= a.tiles[1];
+    }
+    const PairProblem& p = a.p[MULTI ? q : 0];
+    const int per = kGroupM * p.tiles_n;
+    const int g = t / per, m0 = g * kGroupM, gm = min(p.tiles_m - m0, kGroupM), rr = t - g * per;
+    tm = m0 + rr % gm;
+    tn = rr / gm;
+    return true;
 }
 
 // 32 accumulator columns of the warp's lanes (columns past the tile's are read
@@ -168,14 +204,13 @@ __device__ __forceinline__ float4 ld_early(const float* p) {
     asm volatile("ld.global.cs.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
     return v;
 }
-template <bool MX4, bool AMN, bool BMN, int EPI>
+// AMN: A MN-major (0, 1, or 2: as each product says).
+template <bool MX4, int AMN, bool BMN, int EPI>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
-    dense_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
-                      const __grid_constant__ CUtensorMap samap, const __grid_constant__ CUtensorMap sbmap,
-                      const PairArgs a) {
+    dense_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ PairArgs a) {
     using C = PairCfg<MX4>;
     constexpr int ST = C::kStages;
-    const int BN = a.bn;  // up to C::BN
+    constexpr bool MULTI = AMN == 2;
     extern __shared__ uint8_t smem_raw[];
     // the dynamic segment starts at the same address in both CTAs, so the
     // aligned offsets agree
@@ -202,11 +237,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (tid == 64) {
-        prefetch_map(&amap);
-        prefetch_map(&bmap);
-        if (MX4) {
-            prefetch_map(&samap);
-            prefetch_map(&sbmap);
+        for (int i = 0; i < (MULTI ? 3 : MX4 ? 2 : 1); ++i) {
+            if (MULTI && a.tiles[i] == 0) continue;
+            prefetch_map(&maps.a[i]);
+            prefetch_map(&maps.b[i]);
         }
     }
     if (warp == 1) {
@@ -218,116 +252,126 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
     cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    if (!(warp == 0 && a.early_b)) {  // everything up to here touched no global memory
+    if (warp != 0) {  // everything up to here touched no global memory
         pdl_wait();
         pdl_trigger();
     }
-    if (a.reset_status && blockIdx.x == 0 && tid == 0) *a.status = 0;
-    const int total = a.tiles_m * a.tiles_n, step = gridDim.x / 2;
+    if (a.reset_status && blockIdx.x == 0 && tid == 32) *a.status = 0;
 
     if (warp == 0) {
         // ------------------------------------------------------- producer
-        const uint32_t e = elect_one();
-        int st = 0;
-        uint32_t ph = 0;
-        bool ok = true;
-        // bytes of both CTAs' copies of a stage
-        const uint32_t bytes = 2u * uint32_t(kABytes + (BMN ? (BN > 128 ? 16384 : 8192) : BN * 64) +
-                                             (MX4 ? C::kSA + (BN > 128 ? C::kSB : C::kSB / 2) : 0));
-        auto load_b = [&](int tn, int ks, int s) {
-            const uint32_t sb = smem_u32(smem + s * C::kStage) + kABytes, fb = map_rank(smem_u32(&full[s]), 0);
-            const int n0 = EPI == kEpiGate ? tn * (BN / 2) : tn * BN + int(rank) * (BN / 2);
-            if (rank == 0) mbar_expect_tx_e(smem_u32(&full[s]), bytes, e);
-            if (BMN) {
-                tma_3d_pair_e(sb, &bmap, n0, ks * 64, 0, fb, e);
-                if (BN > 128) tma_3d_pair_e(sb + 8192, &bmap, n0 + 64, ks * 64, 0, fb, e);
+        // one thread: a stage's turn (wait, expect, two to four copies) has to
+        // take less than its MMAs, 320 clocks at 160 columns
+        if (elect_one()) {
+            int st = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            const uint32_t stage0 = smem_u32(smem), full0 = map_rank(smem_u32(full), 0);  // the leader's barriers
+            auto load_b = [&](int q, int tn, int ks, int s) {
+                const int BN = a.p[MULTI ? q : 0].bn;
+                const uint32_t sb = stage0 + s * C::kStage + kABytes, fb = full0 + 8 * s;
+                const int n0 = EPI == kEpiGate ? tn * (BN / 2) : tn * BN + int(rank) * (BN / 2);
+                // bytes of both CTAs' copies of a stage
+                if (rank == 0)
+                    mbar_expect_tx(smem_u32(full) + 8 * s,
+                                   2u * uint32_t(kABytes + (BMN ? (BN > 128 ? 16384 : 8192) : BN * 64) +
+                                                 (MX4 ? C::kSA + (BN > 128 ? C::kSB : C::kSB / 2) : 0)));
+                const CUtensorMap* m = &maps.b[MULTI ? q : 0];
+                if (BMN) {
+                    tma_3d_pair(sb, m, n0, ks * 64, 0, fb);
+                    if (BN > 128) tma_3d_pair(sb + 8192, m, n0 + 64, ks * 64, 0, fb);
+                } else {
+                    tma_3d_pair(sb, m, ks * (MX4 ? 128 : 64), n0, EPI == kEpiGate ? int(rank) : 0, fb);
+                }
+            };
+            auto load_a = [&](int q, int tm, int tn, int ks, int s) {
+                const uint32_t sa = stage0 + s * C::kStage, fb = full0 + 8 * s;
+                const int m0 = tm * 256 + int(rank) * 128;
+                const CUtensorMap* m = &maps.a[MULTI ? q : 0];
+                if (AMN == 1 || (MULTI && a.p[MULTI ? q : 0].amn)) {
+                    tma_3d_pair(sa, m, m0, ks * 64, 0, fb);
+                    tma_3d_pair(sa + 8192, m, m0 + 64, ks * 64, 0, fb);
+                } else {
+                    tma_3d_pair(sa, m, ks * (MX4 ? 128 : 64), m0, 0, fb);
+                }
+                if (MX4) {
+                    const uint32_t ss = sa + kABytes + C::kB;
+                    tma_3d_pair(ss, &maps.a[1], 0, (m0 >> 7) * a.chunks + 2 * ks, 0, fb);
+                    // rows of 512 bytes: a chunk of up to 128 tile rows
+                    tma_3d_pair(ss + C::kSA, &maps.b[1], 0, (tn * a.chunks + 2 * ks) * (a.p[0].bn > 128 ? 2 : 1), 0, fb);
+                }
+            };
+            int ks = 0, q, tm, tn;
+            const bool any = tile_at<MULTI>(a, 0, q, tm, tn);
+            if (any && a.p[MULTI ? q : 0].early_b) {
+                // the first stages of B while the kernel before this one drains
+                const int first = min(ST, a.p[MULTI ? q : 0].nks);
+                for (int i = 0; i < first; ++i) load_b(q, tn, i, i);
+                pdl_wait();
+                for (; ks < first; ++ks) load_a(q, tm, tn, ks, ks);
+                if (first == ST) ph = 1;
+                else st = first;
             } else {
-                tma_3d_pair_e(sb, &bmap, ks * (MX4 ? 128 : 64), n0, EPI == kEpiGate ? int(rank) : 0, fb, e);
+                pdl_wait();
             }
-        };
-        auto load_a = [&](int tm, int tn, int ks, int s) {
-            const uint32_t sa = smem_u32(smem + s * C::kStage), fb = map_rank(smem_u32(&full[s]), 0);
-            const int m0 = tm * 256 + int(rank) * 128;
-            if (AMN) {
-                tma_3d_pair_e(sa, &amap, m0, ks * 64, 0, fb, e);
-                tma_3d_pair_e(sa + 8192, &amap, m0 + 64, ks * 64, 0, fb, e);
-            } else {
-                tma_3d_pair_e(sa, &amap, ks * (MX4 ? 128 : 64), m0, 0, fb, e);
+            for (int i = 0; ok && tile_at<MULTI>(a, i, q, tm, tn); ++i) {
+                for (; ks < a.p[MULTI ? q : 0].nks; ++ks) {
+                    if (!mbar_wait(smem_u32(&empty[st]), ph ^ 1u, abort_flag, a.status, kTimeoutNs)) { ok = false; break; }
+                    load_b(q, tn, ks, st);
+                    load_a(q, tm, tn, ks, st);
+                    if (++st == ST) { st = 0; ph ^= 1u; }
+                }
+                ks = 0;
             }
-            if (MX4) {
-                const uint32_t ss = sa + kABytes + C::kB;
-                tma_3d_pair_e(ss, &samap, 0, (m0 >> 7) * a.chunks + 2 * ks, 0, fb, e);
-                // rows of 512 bytes: a chunk of up to 128 tile rows
-                tma_3d_pair_e(ss + C::kSA, &sbmap, 0, (tn * a.chunks + 2 * ks) * (BN > 128 ? 2 : 1), 0, fb, e);
-            }
-        };
-        int ks = 0;
-        if (a.early_b && int(blockIdx.x / 2) < total) {
-            // the first stages of B while the kernel before this one drains
-            int tm, tn;
-            pair_tile(a, blockIdx.x / 2, tm, tn);
-            const int first = min(ST, a.nks);
-            for (int i = 0; i < first; ++i) load_b(tn, i, i);
-            pdl_wait();
-            for (; ks < first; ++ks) load_a(tm, tn, ks, ks);
-            if (first == ST) ph = 1;
-            else st = first;
-        }
-        for (int t = blockIdx.x / 2; ok && t < total; t += step) {
-            int tm, tn;
-            pair_tile(a, t, tm, tn);
-            for (; ks < a.nks; ++ks) {
-                if (!warp_wait(smem_u32(&empty[st]), ph ^ 1u, abort_flag, a.status, kTimeoutNs)) { ok = false; break; }
-                load_b(tn, ks, st);
-                load_a(tm, tn, ks, st);
-                if (++st == ST) { st = 0; ph ^= 1u; }
-            }
-            ks = 0;
         }
     } else if (warp == 1 && rank == 0) {
         // ------------------------------------------------------- MMA issue
-        const uint32_t e = elect_one();
-        int st = 0, acc = 0;
-        uint32_t ph = 0, cph = 0;
-        bool ok = true;
-        const uint32_t idesc = idesc_f16(256, BN, AMN, BMN);
-        const uint32_t tscale = tmem + 2 * C::BN;  // MX4: A chunk 0, 1 (4 columns each), B chunk 0, 1 (8 each)
-        for (int t = blockIdx.x / 2; ok && t < total; t += step) {
-            if (!warp_wait_cluster(smem_u32(&acce[acc]), cph ^ 1u, abort_flag, a.status)) break;
-            tc_fence_after();
-            const uint32_t d = tmem + uint32_t(acc * C::BN);
-            for (int ks = 0; ks < a.nks; ++ks) {
-                if (!warp_wait_cluster(smem_u32(&full[st]), ph, abort_flag, a.status)) { ok = false; break; }
+        if (elect_one()) {
+            int st = 0, acc = 0;
+            uint32_t ph = 0, cph = 0;
+            bool ok = true;
+            const uint32_t tscale = tmem + 2 * C::BN;  // MX4: A chunk 0, 1 (4 columns each), B chunk 0, 1 (8 each)
+            int q, tm, tn;
+            for (int i = 0; ok && tile_at<MULTI>(a, i, q, tm, tn); ++i) {
+                if (!mbar_wait_cluster(smem_u32(&acce[acc]), cph ^ 1u, abort_flag, a.status)) break;
                 tc_fence_after();
-                const uint32_t sa = smem_u32(smem + st * C::kStage), sb = sa + kABytes;
-                const uint32_t acc0 = ks > 0 ? 1u : 0u;
-                if constexpr (MX4) {
-                    const uint32_t ssa = sb + C::kB, ssb = ssa + C::kSA;
+                const int BN = a.p[MULTI ? q : 0].bn, nks = a.p[MULTI ? q : 0].nks;
+                const bool amn = AMN == 1 || (MULTI && a.p[MULTI ? q : 0].amn);
+                const uint32_t idesc = idesc_f16(256, BN, amn, BMN);
+                const uint32_t d = tmem + uint32_t(acc * C::BN);
+                for (int ks = 0; ks < nks; ++ks) {
+                    if (!mbar_wait_cluster(smem_u32(&full[st]), ph, abort_flag, a.status)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t sa = smem_u32(smem + st * C::kStage), sb = sa + kABytes;
+                    const uint32_t acc0 = ks > 0 ? 1u : 0u;
+                    if constexpr (MX4) {
+                        const uint32_t ssa = sb + C::kB, ssb = ssa + C::kSA;
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        cp_scales_pair_e(tscale + 4 * j, desc_scales(ssa + 512 * j), e);
-                        cp_scales_pair_e(tscale + 8 + 8 * j, desc_scales(ssb + (BN > 128 ? 1024 : 512) * j), e);
-                        if (BN > 128) cp_scales_pair_e(tscale + 12 + 8 * j, desc_scales(ssb + 1024 * j + 512), e);
+                        for (int j = 0; j < 2; ++j) {
+                            cp_scales_pair(tscale + 4 * j, desc_scales(ssa + 512 * j));
+                            cp_scales_pair(tscale + 8 + 8 * j, desc_scales(ssb + (BN > 128 ? 1024 : 512) * j));
+                            if (BN > 128) cp_scales_pair(tscale + 12 + 8 * j, desc_scales(ssb + 1024 * j + 512));
+                        }
+                        const uint64_t ad = desc_sw128(sa), bd = desc_sw128(sb);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_mx4_pair(d, ad + uint64_t(2 * kk), bd + uint64_t(2 * kk), idesc_mx4(256, BN, 2 * (kk & 1)),
+                                           tscale + 4 * (kk >> 1), tscale + 8 + 8 * (kk >> 1), kk > 0 ? 1u : acc0);
+                    } else {
+                        const uint64_t ad = amn ? desc_mn128(sa) : desc_sw128(sa);
+                        const uint64_t bd = BMN ? desc_mn128(sb) : desc_sw128(sb);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)  // 16 k: 32 bytes into each line, or 16 lines on
+                            mma_bf16_pair(d, ad + uint64_t((amn ? 128 : 2) * kk), bd + uint64_t((BMN ? 128 : 2) * kk),
+                                            idesc, kk > 0 ? 1u : acc0);
                     }
-                    const uint64_t ad = desc_sw128(sa), bd = desc_sw128(sb);
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_mx4_pair_e(d, ad + uint64_t(2 * kk), bd + uint64_t(2 * kk), idesc_mx4(256, BN, 2 * (kk & 1)),
-                                       tscale + 4 * (kk >> 1), tscale + 8 + 8 * (kk >> 1), kk > 0 ? 1u : acc0, e);
-                } else {
-                    const uint64_t ad = AMN ? desc_mn128(sa) : desc_sw128(sa);
-                    const uint64_t bd = BMN ? desc_mn128(sb) : desc_sw128(sb);
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)  // 16 k: 32 bytes into each line, or 16 lines on
-                        mma_bf16_pair_e(d, ad + uint64_t((AMN ? 128 : 2) * kk), bd + uint64_t((BMN ? 128 : 2) * kk),
-                                        idesc, kk > 0 ? 1u : acc0, e);
+                    mma_commit_pair(smem_u32(&empty[st]));
+                    if (++st == ST) { st = 0; ph ^= 1u; }
                 }
-                mma_commit_pair_e(smem_u32(&empty[st]), e);
-                if (++st == ST) { st = 0; ph ^= 1u; }
+                if (!ok) break;
+                mma_commit_pair(smem_u32(&accf[acc]));
+                if (++acc == 2) { acc = 0; cph ^= 1u; }
             }
-            if (!ok) break;
-            mma_commit_pair_e(smem_u32(&accf[acc]), e);
-            if (++acc == 2) { acc = 0; cph ^= 1u; }
         }
     } else if (warp >= kPEpi0) {
         // ------------------------------------------------------- epilogue
@@ -335,16 +379,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
         uint4* turn = reinterpret_cast<uint4*>(smem + C::kTurnOff + (warp - kPEpi0) * 4096);
         int acc = 0;
         uint32_t cph = 0;
-        for (int t = blockIdx.x / 2; t < total; t += step) {
-            int tm, tn;
-            pair_tile(a, t, tm, tn);
+        int q, tm, tn;
+        for (int i = 0; tile_at<MULTI>(a, i, q, tm, tn); ++i) {
+            const PairProblem& p = a.p[MULTI ? q : 0];
+            const int64_t M = p.M, N = p.N;
+            const int BN = p.bn;
             if (!warp_wait(smem_u32(&accf[acc]), cph, abort_flag, a.status, kTimeoutNs)) break;
             tc_fence_after();
             const uint32_t tb = tmem + (uint32_t(qd * 32) << 16) + uint32_t(acc * C::BN);
             const int64_t m0 = int64_t(tm) * 256 + rank * 128 + qd * 32;
-            const int rows = int(max(int64_t(0), min(int64_t(32), a.M - m0)));
+            const int rows = int(max(int64_t(0), min(int64_t(32), M - m0)));
             if (EPI == kEpiStore) {
-                const int64_t end = min(a.N, int64_t(tn + 1) * BN);
+                const int64_t end = min(N, int64_t(tn + 1) * BN);
                 // 32 columns with the bias of theirs
                 auto fetch = [&](int c, int64_t n, float (&v)[32]) {
                     tmem_f32(tb + uint32_t(c), v);
@@ -363,7 +409,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
                         if (n >= end) break;  // uniform over the warp
                         fetch(c, n, v);
                         put_f32(turn, lane, v);
-                        turn_out<8>(turn, (float*)a.out + m0 * a.N + n, a.N, rows, int(min(int64_t(32), end - n)), a.vec_out,
+                        turn_out<8>(turn, (float*)p.out + m0 * N + n, N, rows, int(min(int64_t(32), end - n)), p.vec_out,
                                     lane);
                     }
                 } else {
@@ -378,16 +424,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
                             pack32(v, w + 4);
                         }
                         turn_put<8>(turn, lane, w);
-                        turn_out<8>(turn, (__nv_bfloat16*)a.out + m0 * a.N + n, a.N, rows, int(min(int64_t(64), end - n)),
-                                    a.vec_out, lane);
+                        turn_out<8>(turn, (__nv_bfloat16*)p.out + m0 * N + n, N, rows, int(min(int64_t(64), end - n)),
+                                    p.vec_out, lane);
                     }
                 }
             } else if (EPI == kEpiGate) {
                 const int bh = BN / 2;
                 for (int c = half * 32; c < bh; c += 64) {
                     const int64_t n = int64_t(tn) * bh + c;
-                    if (n >= a.N) break;
-                    const int cols = int(min(int64_t(min(32, bh - c)), a.N - n));  // a multiple of 8, as N and bh are
+                    if (n >= N) break;
+                    const int cols = int(min(int64_t(min(32, bh - c)), N - n));  // a multiple of 8, as N and bh are
                     float g[32], u[32];
                     tmem_f32(tb + uint32_t(c), g);
                     tmem_f32(tb + uint32_t(bh + c), u);
@@ -396,7 +442,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
                         float bg = 0.0f, bu = 0.0f;
                         if (lane < cols) {
                             bg = __bfloat162float(b[a.interleaved ? 2 * (n + lane) : n + lane]);
-                            bu = __bfloat162float(b[a.interleaved ? 2 * (n + lane) + 1 : a.N + n + lane]);
+                            bu = __bfloat162float(b[a.interleaved ? 2 * (n + lane) + 1 : N + n + lane]);
                         }
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
@@ -405,7 +451,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
                         }
                     }
                     if (a.gu) {
-                        float* gr = a.gu + m0 * 2 * a.N;
+                        float* gr = a.gu + m0 * 2 * N;
                         if (a.interleaved) {
 #pragma unroll
                             for (int k = 0; k < 32; k += 16) {
@@ -416,13 +462,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
                                     w[2 * i + 1] = u[k + i];
                                 }
                                 put_f32(turn, lane, w);
-                                turn_out<8>(turn, gr + 2 * (n + k), 2 * a.N, rows, 2 * (cols - k), true, lane);
+                                turn_out<8>(turn, gr + 2 * (n + k), 2 * N, rows, 2 * (cols - k), true, lane);
                             }
                         } else {
                             put_f32(turn, lane, g);
-                            turn_out<8>(turn, gr + n, 2 * a.N, rows, cols, true, lane);
+                            turn_out<8>(turn, gr + n, 2 * N, rows, cols, true, lane);
                             put_f32(turn, lane, u);
-                            turn_out<8>(turn, gr + a.N + n, 2 * a.N, rows, cols, true, lane);
+                            turn_out<8>(turn, gr + N + n, 2 * N, rows, cols, true, lane);
                         }
                     }
 #pragma unroll
@@ -430,12 +476,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
                     uint4 w[4];
                     pack32(g, w);
                     turn_put<4>(turn, lane, w);
-                    turn_out<4>(turn, (__nv_bfloat16*)a.out + m0 * a.N + n, a.N, rows, cols, true, lane);
+                    turn_out<4>(turn, (__nv_bfloat16*)p.out + m0 * N + n, N, rows, cols, true, lane);
                 }
             } else {
                 // dh turned to eight lanes a row, four columns each, beside g and u
                 const int j = lane & 7, r0 = lane >> 3;
-                const int64_t end = min(a.N, int64_t(tn + 1) * BN);
+                const int64_t end = min(N, int64_t(tn + 1) * BN);
                 for (int c = half * 32; c < BN; c += 64) {
                     const int64_t n = int64_t(tn) * BN + c;
                     if (n >= end) break;
@@ -446,18 +492,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
                     const int mine = col < end ? rows - r0 : 0;  // N is a multiple of 8: whole fours
                     if (mine > 0) {
                         // interleaved: g, u, g, u, ...; else fours of g and of u, N apart
-                        const int64_t at = (m0 + r0) * 2 * a.N + (a.interleaved ? 2 * col : col);
-                        const int64_t apart = a.interleaved ? 4 : a.N;
+                        const int64_t at = (m0 + r0) * 2 * N + (a.interleaved ? 2 * col : col);
+                        const int64_t apart = a.interleaved ? 4 : N;
                         const float* gr = a.gu + at;
                         __nv_bfloat16* dr = (__nv_bfloat16*)a.dgu + at;
-                        __nv_bfloat16* hp = (__nv_bfloat16*)a.out + (m0 + r0) * a.N + col;
+                        __nv_bfloat16* hp = (__nv_bfloat16*)p.out + (m0 + r0) * N + col;
 #pragma unroll
                         for (int i0 = 0; i0 < 8; i0 += 4) {
                             float4 x[4], y[4];
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
                                 // a row past the end reads the last one: no branch keeps a load back
-                                const float* r = gr + int64_t(min(4 * (i0 + i), (mine - 1) & ~3)) * 2 * a.N;
+                                const float* r = gr + int64_t(min(4 * (i0 + i), (mine - 1) & ~3)) * 2 * N;
                                 x[i] = ld_early(r);
                                 y[i] = ld_early(r + apart);
                             }
@@ -480,16 +526,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
                                     du[k] = dh[k] * hu;
                                 }
                                 if (row < mine) {
-                                    *reinterpret_cast<uint2*>(hp + int64_t(row) * a.N) =
+                                    *reinterpret_cast<uint2*>(hp + int64_t(row) * N) =
                                         make_uint2(pack_bf16(h[0], h[1]), pack_bf16(h[2], h[3]));
-                                    __nv_bfloat16* d = dr + int64_t(row) * 2 * a.N;
+                                    __nv_bfloat16* d = dr + int64_t(row) * 2 * N;
                                     if (a.interleaved) {
                                         *reinterpret_cast<uint4*>(d) =
                                             make_uint4(pack_bf16(dg[0], du[0]), pack_bf16(dg[1], du[1]),
                                                        pack_bf16(dg[2], du[2]), pack_bf16(dg[3], du[3]));
                                     } else {
                                         *reinterpret_cast<uint2*>(d) = make_uint2(pack_bf16(dg[0], dg[1]), pack_bf16(dg[2], dg[3]));
-                                        *reinterpret_cast<uint2*>(d + a.N) =
+                                        *reinterpret_cast<uint2*>(d + N) =
                                             make_uint2(pack_bf16(du[0], du[1]), pack_bf16(du[2], du[3]));
                                     }
                                 }
@@ -518,15 +564,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
     }
 }
 
-template <bool MX4, bool AMN, bool BMN, int EPI>
-cudaError_t launch_one(const CUtensorMap (&maps)[4], const PairArgs& a, cudaStream_t st) {
+template <bool MX4, int AMN, bool BMN, int EPI>
+cudaError_t launch_one(const PairMaps& maps, const PairArgs& a, cudaStream_t st) {
     constexpr auto kern = dense_pair_kernel<MX4, AMN, BMN, EPI>;
     cudaError_t e = raise_smem<kern>(PairCfg<MX4>::kSmem);
     if (e != cudaSuccess) return e;
-    const int64_t tiles = int64_t(a.tiles_m) * a.tiles_n, pairs = sm_count() / 2;
+    const int64_t tiles = int64_t(a.tiles[0]) + a.tiles[1] + a.tiles[2], pairs = sm_count() / 2;
     const int grid = 2 * int(tiles < pairs ? tiles : pairs);
-    return launch_kernel(kern, dim3(unsigned(grid)), dim3(kPThreads), PairCfg<MX4>::kSmem, st, true, maps[0], maps[1],
-                         maps[2], maps[3], a);
+    return launch_kernel(kern, dim3(unsigned(grid)), dim3(kPThreads), PairCfg<MX4>::kSmem, st, true, maps, a);
 }
 
 // Tile columns: the widest (256; 240 for MX4) where the tiles fill many rounds
@@ -537,12 +582,14 @@ cudaError_t launch_one(const CUtensorMap (&maps)[4], const PairArgs& a, cudaStre
 // columns) against 256 throughout: forward 56.7 against 67.6 us, training step
 // 194 against 217 us; 160 columns at T = 4096, H = 4096, I = 14336 (where the
 // rule keeps 256) take 3792 us against 3120.
-int pair_width(int64_t tiles_m, int64_t n, bool mx4) {
+// A second product of the same launch counts its tiles too.
+int pair_width(int64_t tiles_m, int64_t n, bool mx4, int64_t tiles_m2 = 0, int64_t n2 = 0) {
     constexpr int64_t kPairs = 74;
     int best = 0;
     int64_t cost = INT64_MAX;
     for (int bn = mx4 ? PairCfg<true>::BN : 256; bn >= 128; bn = (bn - 1) / 32 * 32) {
-        const int64_t tiles = tiles_m * ((n + bn - 1) / bn), c = (tiles + kPairs - 1) / kPairs * (bn + 256);
+        const int64_t tiles = tiles_m * ((n + bn - 1) / bn) + tiles_m2 * ((n2 + bn - 1) / bn);
+        const int64_t c = (tiles + kPairs - 1) / kPairs * (bn + 256);
         if (c < cost) {
             cost = c;
             best = bn;
@@ -568,32 +615,52 @@ size_t dense_pair_workspace(int64_t M, int64_t N, int64_t K) {
     return size_t(up256(a.bytes()) + up256(b.bytes()));
 }
 
-cudaError_t launch_dense_pair(const DenseArgs& d, bool early_b, cudaStream_t st) {
+namespace {
+
+// Sizes and output of product q with tiles of bn columns; false when there are
+// too many tiles.
+bool set_problem(PairArgs& a, int q, const DenseArgs& d, int bn, bool early) {
+    PairProblem& p = a.p[q];
     const bool gate = d.epi == kEpiGate;
+    p.M = d.M;
+    p.N = gate ? d.N / 2 : d.N;
+    p.tiles_m = int((d.M + 255) / 256);
+    p.bn = bn;
+    const int64_t w = gate ? bn / 2 : bn, tn = (p.N + w - 1) / w;
+    p.nks = int((d.K + (d.mx4 ? 255 : 63)) / (d.mx4 ? 256 : 64));
+    p.amn = d.a.k_step != 1;
+    p.early_b = early;
+    p.vec_out = d.N % (d.out_f32 ? 4 : 8) == 0 && (reinterpret_cast<uintptr_t>(d.out) & 15) == 0;
+    p.out = d.out;
+    if (p.tiles_m * tn > (int64_t(1) << 28)) return false;
+    p.tiles_n = int(tn);
+    a.tiles[q] = p.tiles_m * int(tn);
+    return true;
+}
+
+cudaError_t bf16_maps(PairMaps& m, int q, const DenseArgs& d, const PairProblem& p) {
+    cudaError_t e = encode_map(&m.a[q], bf16_spec(d.a, d.M, d.K, 128, 0));
+    if (e != cudaSuccess) return e;
+    if (d.epi != kEpiGate) return encode_map(&m.b[q], bf16_spec(d.b, d.N, d.K, uint32_t(p.bn / 2), 0));
+    DenseOperand w = d.b;  // gate and up rows: every other row, or the two halves
+    if (d.interleaved) w.row *= 2;
+    return encode_map(&m.b[q], bf16_spec(w, p.N, d.K, uint32_t(p.bn / 2), d.interleaved ? d.b.row : p.N * d.b.row));
+}
+
+}  // namespace
+
+cudaError_t launch_dense_pair(const DenseArgs& d, bool early, cudaStream_t st) {
     PairArgs a{};
-    a.M = d.M;
-    a.N = gate ? d.N / 2 : d.N;
-    a.K = d.K;
-    a.tiles_m = int((d.M + 255) / 256);
-    const int BN = pair_width(a.tiles_m, d.N, d.mx4 != 0);
-    a.bn = BN;
-    const int64_t tn = (a.N + (gate ? BN / 2 : BN) - 1) / (gate ? BN / 2 : BN);
-    if (int64_t(a.tiles_m) * tn > (int64_t(1) << 30)) return cudaErrorInvalidValue;
-    a.tiles_n = int(tn);
-    a.nks = int((d.K + (d.mx4 ? 255 : 63)) / (d.mx4 ? 256 : 64));
-    a.epi = d.epi;
+    if (!set_problem(a, 0, d, pair_width((d.M + 255) / 256, d.N, d.mx4 != 0), early)) return cudaErrorInvalidValue;
     a.out_f32 = d.out_f32;
     a.interleaved = d.interleaved;
     a.bias = d.bias;
-    a.out = d.out;
     a.gu = d.gu;
     a.dgu = d.dgu;
     a.gate = d.gate;
     a.status = d.status;
     a.reset_status = d.reset_status;
-    a.early_b = early_b;
-    a.vec_out = d.N % (d.out_f32 ? 4 : 8) == 0 && (reinterpret_cast<uintptr_t>(d.out) & 15) == 0;
-    CUtensorMap maps[4] = {};
+    PairMaps maps = {};
     cudaError_t e;
     if (d.mx4) {
         if (!d.scratch) return cudaErrorInvalidValue;
@@ -601,8 +668,8 @@ cudaError_t launch_dense_pair(const DenseArgs& d, bool early_b, cudaStream_t st)
         dense_pair_tiles(d.M, d.N, d.K, d.scratch, &t[0], &t[1]);
         a.chunks = t[0].chunks;
         for (int i = 0; i < 2; ++i) {
-            const MapSpec s = i ? mx4_spec(d.b.p, d.N, d.K, uint32_t(BN / 2)) : mx4_spec(d.a.p, d.M, d.K, 128);
-            if ((e = encode_map(&maps[i], s)) != cudaSuccess) return e;
+            const MapSpec s = i ? mx4_spec(d.b.p, d.N, d.K, uint32_t(a.p[0].bn / 2)) : mx4_spec(d.a.p, d.M, d.K, 128);
+            if ((e = encode_map(i ? &maps.b[0] : &maps.a[0], s)) != cudaSuccess) return e;
             MapSpec sc{};
             sc.p = t[i].out;
             sc.type = CU_TENSOR_MAP_DATA_TYPE_INT32;
@@ -613,26 +680,40 @@ cudaError_t launch_dense_pair(const DenseArgs& d, bool early_b, cudaStream_t st)
             sc.box[0] = 128;
             sc.box[1] = uint32_t(2 * t[i].subs());  // a stage's two chunks
             sc.box[2] = 1;
-            if ((e = encode_map(&maps[2 + i], sc)) != cudaSuccess) return e;
+            if ((e = encode_map(i ? &maps.b[1] : &maps.a[1], sc)) != cudaSuccess) return e;
         }
-        return launch_one<true, false, false, kEpiStore>(maps, a, st);
+        return launch_one<true, 0, false, kEpiStore>(maps, a, st);
     }
-    if ((e = encode_map(&maps[0], bf16_spec(d.a, d.M, d.K, 128, 0))) != cudaSuccess) return e;
-    if (gate) {  // gate and up rows: every other row, or the two halves
-        DenseOperand w = d.b;
-        if (d.interleaved) w.row *= 2;
-        e = encode_map(&maps[1], bf16_spec(w, a.N, d.K, uint32_t(BN / 2), d.interleaved ? d.b.row : a.N * d.b.row));
-    } else {
-        e = encode_map(&maps[1], bf16_spec(d.b, d.N, d.K, uint32_t(BN / 2), 0));
+    if ((e = bf16_maps(maps, 0, d, a.p[0])) != cudaSuccess) return e;
+    if (d.epi == kEpiGate) return launch_one<false, 0, false, kEpiGate>(maps, a, st);
+    if (d.epi == kEpiGateBwd) return launch_one<false, 0, true, kEpiGateBwd>(maps, a, st);
+    return launch_one<false, 0, false, kEpiStore>(maps, a, st);
+}
+
+cudaError_t launch_dense_pairs(const DenseArgs* first, const DenseArgs* second, const DenseArgs* third, bool early3,
+                               cudaStream_t st) {
+    PairArgs a{};
+    PairMaps maps = {};
+    const DenseArgs* d[3] = {first, second, third};
+    const int64_t m1 = second ? (second->M + 255) / 256 : 0, m2 = third ? (third->M + 255) / 256 : 0;
+    const int width = pair_width(m1, second ? second->N : 0, false, m2, third ? third->N : 0);
+    for (int q = 0; q < 3; ++q) {
+        if (!d[q]) continue;
+        const int bn = q == 0 ? pair_width((d[0]->M + 255) / 256, d[0]->N, false) : width;
+        if (!set_problem(a, q, *d[q], bn, q == 2 ? early3 : true)) return cudaErrorInvalidValue;
+        const cudaError_t e = bf16_maps(maps, q, *d[q], a.p[q]);
+        if (e != cudaSuccess) return e;
+        a.status = d[q]->status;
     }
-    if (e != cudaSuccess) return e;
-    const bool amn = d.a.k_step != 1, bmn = d.b.k_step != 1;
-    maps[2] = maps[3] = maps[0];
-    if (gate) return launch_one<false, false, false, kEpiGate>(maps, a, st);
-    if (d.epi == kEpiGateBwd) return launch_one<false, false, true, kEpiGateBwd>(maps, a, st);
-    if (amn) return launch_one<false, true, true, kEpiStore>(maps, a, st);
-    return bmn ? launch_one<false, false, true, kEpiStore>(maps, a, st)
-               : launch_one<false, false, false, kEpiStore>(maps, a, st);
+    const int D = a.tiles[0], W = a.tiles[1] + a.tiles[2], pairs = sm_count() / 2;
+    const int short_of = D && W && D + W > pairs && D % pairs ? pairs - D % pairs : 0;  // pairs with one fewer long tile
+    if (short_of) {
+        const PairProblem& s = second ? a.p[1] : a.p[2];
+        const int64_t head = int64_t(a.p[0].nks) * (a.p[0].bn + 256) / (int64_t(s.nks) * (s.bn + 256));
+        const int64_t most = (W + short_of - 1) / short_of;
+        a.head = int(head < most ? head : most);
+    }
+    return launch_one<false, 2, true, kEpiStore>(maps, a, st);
 }
 
 }  // namespace qmoe

@@ -29,31 +29,33 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
-// Bounded wait by a whole warp on a phase that the cluster's other CTAs
-// complete (acquire at cluster scope).
-__device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+// Bounded wait of one thread on a phase that the cluster's other CTAs complete
+// (acquire at cluster scope). The clock is not read unless the first try fails.
+__device__ __forceinline__ bool mbar_try_cluster(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n.reg .pred p;\nmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
+        "selp.b32 %0, 1, 0, p;\n}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity), "r"(kSuspendNs)
+        : "memory");
+    return done != 0;
+}
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                                   int32_t* status) {
+    if (mbar_try_cluster(bar, parity)) return true;
     const uint64_t t0 = now_ns();
-    bool ok = false;
     for (uint32_t spin = 1;; ++spin) {
-        uint32_t done;
-        asm volatile(
-            "{\n.reg .pred p;\nmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
-            "selp.b32 %0, 1, 0, p;\n}"
-            : "=r"(done)
-            : "r"(bar), "r"(parity), "r"(kSuspendNs)
-            : "memory");
-        if (done) { ok = true; break; }
+        if (mbar_try_cluster(bar, parity)) return true;
         if ((spin & 15u) == 0u) {
-            if (*abort_flag) break;
+            if (*abort_flag) return false;
             if (now_ns() - t0 > kTimeoutNs) {
                 *abort_flag = 1;
                 atomicExch(status, int32_t(QMOE_TIMEOUT));
-                break;
+                return false;
             }
         }
     }
-    return __all_sync(0xffffffffu, ok);
 }
 
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
@@ -62,50 +64,42 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
 
 // TMA load by one CTA of a pair, completing on a barrier that may be the
 // other CTA's (cluster address).
-__device__ __forceinline__ void tma_3d_pair_e(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar,
-                                              uint32_t e) {
+__device__ __forceinline__ void tma_3d_pair(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
     asm volatile(
-        "{\n.reg .pred q;\nsetp.ne.b32 q, %6, 0;\n"
-        "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], "
-        "[%1, {%2, %3, %4}], [%5];\n}" ::"r"(dst),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar), "r"(e)
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, "
+        "{%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
 
 // Arrive on the same barrier of both CTAs of the pair once the MMAs issued so
 // far have completed.
-__device__ __forceinline__ void mma_commit_pair_e(uint32_t bar, uint32_t e) {
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
     asm volatile(
-        "{\n.reg .pred q;\n.reg .b16 m;\nsetp.ne.b32 q, %1, 0;\nmov.b16 m, 3;\n"
-        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n}" ::"r"(
-            bar),
-        "r"(e)
+        "{\n.reg .b16 m;\nmov.b16 m, 3;\n"
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n}" ::"r"(bar)
         : "memory");
 }
 
-__device__ __forceinline__ void mma_bf16_pair_e(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t acc,
-                                                uint32_t e) {
+__device__ __forceinline__ void mma_bf16_pair(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n.reg .pred p, q;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 q, %5, 0;\n"
-        "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-        "l"(ad), "l"(bd), "r"(idesc), "r"(acc), "r"(e));
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(ad), "l"(bd), "r"(idesc), "r"(acc));
 }
 
-__device__ __forceinline__ void mma_mx4_pair_e(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t sa,
-                                               uint32_t sb, uint32_t acc, uint32_t e) {
+__device__ __forceinline__ void mma_mx4_pair(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t sa,
+                                             uint32_t sb, uint32_t acc) {
     asm volatile(
-        "{\n.reg .pred p, q;\nsetp.ne.b32 p, %6, 0;\nsetp.ne.b32 q, %7, 0;\n"
-        "@q tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),
-        "l"(ad), "l"(bd), "r"(idesc), "r"(sa), "r"(sb), "r"(acc), "r"(e));
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %6, 0;\n"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),
+        "l"(ad), "l"(bd), "r"(idesc), "r"(sa), "r"(sb), "r"(acc));
 }
 
 // 32 rows x 16 bytes of scales from shared memory to 4 tensor-memory columns
 // of every lane quarter, in both CTAs of the pair.
-__device__ __forceinline__ void cp_scales_pair_e(uint32_t t, uint64_t sdesc, uint32_t e) {
-    asm volatile(
-        "{\n.reg .pred q;\nsetp.ne.b32 q, %2, 0;\n@q tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n}" ::"r"(t),
-        "l"(sdesc), "r"(e)
-        : "memory");
+__device__ __forceinline__ void cp_scales_pair(uint32_t t, uint64_t sdesc) {
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(t), "l"(sdesc) : "memory");
 }
 
 // The one-CTA forms.
