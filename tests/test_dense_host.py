@@ -62,6 +62,24 @@ def test_mx4_linear_refuses(q, kw, status):
         assert q.lib.qmoe_dense_last_error()
 
 
+ROWS = [
+    (dict(T=-1), INVALID), (dict(N=0), INVALID), (dict(K=40), INVALID), (dict(dtype=2), INVALID),
+    (dict(T=1 << 31), UNSUPPORTED), (dict(T=0, x=None, y=None, work=None), OK), (dict(ldx=63), INVALID),
+    (dict(ldx=68), INVALID), (dict(x=None), INVALID), (dict(x=A + 8), INVALID), (dict(wc=None), INVALID),
+    (dict(ws=None), INVALID), (dict(wc=A + 4), INVALID), (dict(ws=A + 1), INVALID), (dict(y=None), INVALID),
+    (dict(y=A + 1), INVALID), (dict(bias=A + 1), INVALID), (dict(work=None), INVALID), (dict(work=A + 64), INVALID),
+    (dict(size=256), INVALID),
+]
+
+
+@pytest.mark.parametrize("kw,status", ROWS, ids=[str(i) for i in range(len(ROWS))])
+def test_mx4_linear_rows_refuses(q, kw, status):
+    a = dict(T=4, N=8, K=64, x=A, ldx=64, wc=A, ws=A, bias=None, y=A, dtype=1, work=A, size=1 << 40)
+    a.update(kw)
+    assert q.lib.qmoe_mx4_linear_rows(a["T"], a["N"], a["K"], a["x"], a["ldx"], a["wc"], a["ws"], a["bias"], a["y"],
+                                      a["dtype"], a["work"], a["size"], None) == status
+
+
 def _ffn(q, **kw):
     base = dict(hidden_size=64, inter_size=128, activation_type=3, swiglu_fusion=2, act_dtype=1)
     base.update(kw)
@@ -127,6 +145,8 @@ def test_config_layout_and_sizes(q):
     assert size(c, -1, 0) == 0
     assert q.lib.qmoe_mx4_linear_workspace_size(4, 8, 64) >= 256
     assert q.lib.qmoe_mx4_linear_workspace_size(4, 8, 65) == 0
+    assert q.lib.qmoe_mx4_linear_rows_workspace_size(300, 8, 64) > q.lib.qmoe_mx4_linear_workspace_size(300, 8, 64) > 256
+    assert q.lib.qmoe_mx4_linear_rows_workspace_size(4, 0, 64) == 0
 
 
 def test_tensor_checks():
@@ -148,6 +168,16 @@ def test_tensor_checks():
         dense.mx4_linear(c, s, c, s, bias=torch.zeros(3, dtype=bf))
     with pytest.raises(ValueError):
         dense.mx4_linear(c, s, c, s, bias=torch.zeros(4))
+    with pytest.raises(ValueError):                      # on the CPU
+        dense.mx4_quantize(torch.zeros(4, 64))
+    with pytest.raises(ValueError):
+        dense.mx4_linear(c, s, c, s)
+    lin = dense.MX4Linear(c, s, torch.zeros(4, dtype=bf))
+    for x in (torch.zeros(2, 64, dtype=bf), torch.zeros(2, 32, dtype=bf), torch.zeros(2, 64, dtype=torch.float16)):
+        with pytest.raises(ValueError):
+            lin(x)
+    with pytest.raises(ValueError):
+        dense.MX4Linear(c, s, torch.zeros(5, dtype=bf))
     with pytest.raises(qmoe.QMoEError):
         dense.GatedFFN(60, 64)
     layer = dense.GatedFFN(64, 128)

@@ -149,6 +149,28 @@ def test_mx4_linear_uneven_scales_and_zero_rows(dense):
     assert not y[5].any() and not y[:, 7].any()
 
 
+@pytest.mark.parametrize("dtype", [BF, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("T,N,K", [(1, 200, 4096), (33, 130, 96), (64, 300, 992), (65, 300, 992), (129, 640, 1408),
+                                   (300, 1030, 2880), (700, 260, 32), (1025, 700, 544)])
+def test_mx4_linear_on_dense_rows(dense, T, N, K, dtype):
+    """The call that rounds its rows equals rounding first: contiguous, strided
+    and misaligned rows, with an all-zero row and a NaN."""
+    n = _gen(T + K)
+    base = n(T, K + 64).to(dtype)
+    base[T // 2] = 0.0
+    if T > 2:
+        base[2, 40] = math.nan
+    lin = dense.MX4Linear.from_weights(n(N, K) / math.sqrt(K), n(N).to(dtype))
+    for x in (base[:, :K].contiguous(), base[:, 32:32 + K], base[:, 1:1 + K]):
+        y = lin(x)
+        codes, scales = dense.mx4_quantize(x)
+        assert torch.equal(codes, ref.mx4_quantize(x)[0])
+        want = dense.mx4_linear(codes, scales, lin.w_codes, lin.w_scales, lin.bias, dtype)
+        assert torch.equal(torch.isnan(y), torch.isnan(want)) and torch.equal(y.nan_to_num(), want.nan_to_num())
+        ref_y, bound = ref.mx4_linear(ref.mx4_values(codes, scales), ref.mx4_values(lin.w_codes, lin.w_scales), lin.bias, dtype)
+        within(y, ref_y, torch.nan_to_num(bound))
+
+
 @pytest.mark.parametrize("T", [1, 20, 300])
 def test_mx4_linear_nan_scales_stay_in_their_rows(dense, T):
     n = _gen(4)
@@ -193,18 +215,34 @@ def test_dense_calls_stay_inside_their_workspaces(dense, T):
         torch.cuda.synchronize()
         assert (buf[:256] == 0xA5).all() and (buf[256 + n:] == 0xA5).all()
 
-    out, y2 = torch.empty(T, 1000, dtype=BF, device="cuda"), torch.empty_like(y)
+    # outputs between canaries too
+    frames = []
+
+    def framed(like):
+        buf = torch.full((like.numel() + 64,), -7.0, dtype=like.dtype, device="cuda")
+        frames.append((buf, like.numel()))
+        return buf[32:32 + like.numel()].view(like.shape)
+
+    out, y2, gu2 = framed(torch.empty(T, 1000, dtype=BF)), framed(y), framed(gu)
     guarded(qmoe.qmoe_mx4_linear_workspace_size(T, 1000, 4096), lambda ws, n: qmoe.qmoe_mx4_linear(
         T, 1000, 4096, *xq, *wq, b, out, qmoe.DTYPE_BF16, ws, n))
     assert torch.equal(out, dense.mx4_linear(*xq, *wq, b))
     guarded(qmoe.qmoe_gated_ffn_workspace_size(layer.cfg, T, False), lambda ws, n: qmoe.qmoe_gated_ffn_forward(
-        layer.cfg, T, p["x"], p["w1"], p["b1"], p["w2"], p["b2"], None, y2, ws, n))
-    assert torch.equal(y, y2)
-    g = [torch.empty_like(t) for t in full]
+        layer.cfg, T, p["x"], p["w1"], p["b1"], p["w2"], p["b2"], gu2, y2, ws, n))
+    assert torch.equal(y, y2) and torch.equal(gu, gu2)
+    x32 = p["x"].float()[:, :256].contiguous()
+    lin = dense.MX4Linear.from_weights(_gen(1)(1000, 256), None)
+    out2 = framed(torch.empty(T, 1000))
+    guarded(qmoe.qmoe_mx4_linear_rows_workspace_size(T, 1000, 256), lambda ws, n: qmoe.qmoe_mx4_linear_rows(
+        T, 1000, 256, x32, 256, lin.w_codes, lin.w_scales, None, out2, qmoe.DTYPE_F32, ws, n))
+    assert torch.equal(out2, lin(x32))
+    g = [framed(t) for t in full]
     guarded(qmoe.qmoe_gated_ffn_workspace_size(layer.cfg, T, True), lambda ws, n: qmoe.qmoe_gated_ffn_backward(
         layer.cfg, T, dy, p["x"], p["w1"], p["w2"], gu, g[0], g[1], g[3], g[2], g[4], ws, n))
     for a, b in zip(g, full):
         assert torch.equal(a, b)
+    for buf, n in frames:
+        assert (buf[:32] == -7.0).all() and (buf[32 + n:] == -7.0).all()
 
 
 def test_mx4_linear_layer(dense):
