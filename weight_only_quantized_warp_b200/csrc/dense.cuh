@@ -16,9 +16,13 @@ namespace qmoe {
 //   kGateErf       the normal distribution function
 //   kGateStep      1 for g > 0, else 0 (ReLU)
 //   kGateOne       1
-// so that one short piece of code, unrolled over a thread's elements, serves
-// every activation (six inlined bodies overflowed the instruction cache: the
-// gradient epilogue then took 60 us for one tile's rows, all of it fetching).
+// The wide epilogues branch on s once per block of elements (with_gate_mode), so
+// the code they run is short and straight: with the branch inside the unrolled
+// element loop they were bound by instruction fetches (128 x 80 columns of h
+// took 10 us against 5, one tile of the backward pass 60 us with all six
+// activations inlined). The streaming kernel's few elements branch one by one:
+// copies of its code for each s measured slower (a token's block 64 against 61
+// us, a training step of 64 tokens 45 against 43).
 enum : int { kGateSigmoid = 0, kGateErf = 1, kGateStep = 2, kGateOne = 3 };
 struct GateParams {
     int mode;
@@ -29,39 +33,60 @@ struct GateParams {
 __device__ __forceinline__ float clamp_hi(float v, float hi) { return v > hi ? hi : v; }
 __device__ __forceinline__ float clamp_lo(float v, float lo) { return v < lo ? lo : v; }
 
-// act(g), and its slope when asked for: s + g s'(g). Fast exponentials and
+// act(g), and its slope when asked for: s + g s'(g). MODE is the mode, or -1 to
+// branch here. Fast exponentials and
 // division: about 2^-21 relative, far inside the bf16 rounding that every
 // result goes through.
-template <bool SLOPE>
+template <int MODE>
+__device__ __forceinline__ bool gate_is(const GateParams& p, int mode) {
+    return MODE < 0 ? p.mode == mode : MODE == mode;
+}
+template <int MODE, bool SLOPE>
 __device__ __forceinline__ float gate_act(const GateParams& p, float g, float& slope) {
-    if (p.mode == kGateSigmoid) {
+    if (gate_is<MODE>(p, kGateSigmoid)) {
         const float g2 = g * g, s = __fdividef(1.0f, 1.0f + __expf(-g * fmaf(p.c3, g2, p.c1)));
         if (SLOPE) slope = fmaf(g * fmaf(3.0f * p.c3, g2, p.c1), s * (1.0f - s), s);
         return g * s;
     }
-    if (p.mode == kGateErf) {
+    if (gate_is<MODE>(p, kGateErf)) {
         const float s = 0.5f * (1.0f + erff(g * 0.70710678118654752f));
         if (SLOPE) slope = fmaf(g * 0.39894228040143268f, __expf(-0.5f * g * g), s);
         return g * s;
     }
-    const bool on = p.mode == kGateOne || g > 0.0f;
+    const bool on = gate_is<MODE>(p, kGateOne) || g > 0.0f;
     if (SLOPE) slope = on ? 1.0f : (g <= 0.0f ? 0.0f : g);
     return on || !(g <= 0.0f) ? g : 0.0f;
 }
 
+template <int MODE>
 __device__ __forceinline__ float gate_value(const GateParams& p, float g, float u) {
     float none;
-    return gate_act<false>(p, clamp_hi(g, p.limit), none) * (clamp_lo(clamp_hi(u, p.limit), -p.limit) + p.beta);
+    return gate_act<MODE, false>(p, clamp_hi(g, p.limit), none) *
+           (clamp_lo(clamp_hi(u, p.limit), -p.limit) + p.beta);
 }
 
 // h and its derivatives by g and u (0 beyond a clamp).
+template <int MODE>
 __device__ __forceinline__ float gate_slopes(const GateParams& p, float g, float u, float& hg, float& hu) {
     float slope;
-    const float a = gate_act<true>(p, clamp_hi(g, p.limit), slope);
+    const float a = gate_act<MODE, true>(p, clamp_hi(g, p.limit), slope);
     const float f = clamp_lo(clamp_hi(u, p.limit), -p.limit) + p.beta;
     hg = g > p.limit ? 0.0f : slope * f;
     hu = fabsf(u) > p.limit ? 0.0f : a;
     return a * f;
+}
+
+// f(GateMode<mode of p>()).
+template <int MODE>
+struct GateMode {
+    static constexpr int value = MODE;
+};
+template <typename F>
+__device__ __forceinline__ void with_gate_mode(const GateParams& p, F&& f) {
+    if (p.mode == kGateSigmoid) f(GateMode<kGateSigmoid>());
+    else if (p.mode == kGateErf) f(GateMode<kGateErf>());
+    else if (p.mode == kGateStep) f(GateMode<kGateStep>());
+    else f(GateMode<kGateOne>());
 }
 
 // 4 NW consecutive scales of a row of `pitch` scales, from scale k0 on (a

@@ -471,8 +471,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
                             turn_out<8>(turn, gr + N + n, 2 * N, rows, cols, true, lane);
                         }
                     }
+                    with_gate_mode(a.gate, [&](auto mode) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) g[i] = gate_value(a.gate, g[i], u[i]);
+                        for (int i = 0; i < 32; ++i) g[i] = gate_value<decltype(mode)::value>(a.gate, g[i], u[i]);
+                    });
                     uint4 w[4];
                     pack32(g, w);
                     turn_put<4>(turn, lane, w);
@@ -518,13 +520,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
                                 const float u[4] = {a.interleaved ? x[i].y : y[i].x, a.interleaved ? x[i].w : y[i].y,
                                                     a.interleaved ? y[i].y : y[i].z, y[i].w};
                                 float h[4], dg[4], du[4];
+                                with_gate_mode(a.gate, [&](auto mode) {
 #pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    float hg, hu;
-                                    h[k] = gate_slopes(a.gate, g[k], u[k], hg, hu);
-                                    dg[k] = dh[k] * hg;
-                                    du[k] = dh[k] * hu;
-                                }
+                                    for (int k = 0; k < 4; ++k) {
+                                        float hg, hu;
+                                        h[k] = gate_slopes<decltype(mode)::value>(a.gate, g[k], u[k], hg, hu);
+                                        dg[k] = dh[k] * hg;
+                                        du[k] = dh[k] * hu;
+                                    }
+                                });
                                 if (row < mine) {
                                     *reinterpret_cast<uint2*>(hp + int64_t(row) * N) =
                                         make_uint2(pack_bf16(h[0], h[1]), pack_bf16(h[2], h[3]));
