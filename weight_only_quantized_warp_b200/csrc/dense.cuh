@@ -58,35 +58,46 @@ __device__ __forceinline__ float gate_act(const GateParams& p, float g, float& s
     return on || !(g <= 0.0f) ? g : 0.0f;
 }
 
-template <int MODE>
+// CLAMP false: the limit is +inf.
+template <int MODE, bool CLAMP>
 __device__ __forceinline__ float gate_value(const GateParams& p, float g, float u) {
     float none;
-    return gate_act<MODE, false>(p, clamp_hi(g, p.limit), none) *
-           (clamp_lo(clamp_hi(u, p.limit), -p.limit) + p.beta);
+    if (CLAMP) {
+        g = clamp_hi(g, p.limit);
+        u = clamp_lo(clamp_hi(u, p.limit), -p.limit);
+    }
+    return gate_act<MODE, false>(p, g, none) * (u + p.beta);
 }
 
 // h and its derivatives by g and u (0 beyond a clamp).
-template <int MODE>
+template <int MODE, bool CLAMP>
 __device__ __forceinline__ float gate_slopes(const GateParams& p, float g, float u, float& hg, float& hu) {
     float slope;
-    const float a = gate_act<MODE, true>(p, clamp_hi(g, p.limit), slope);
-    const float f = clamp_lo(clamp_hi(u, p.limit), -p.limit) + p.beta;
-    hg = g > p.limit ? 0.0f : slope * f;
-    hu = fabsf(u) > p.limit ? 0.0f : a;
+    const float a = gate_act<MODE, true>(p, CLAMP ? clamp_hi(g, p.limit) : g, slope);
+    const float f = (CLAMP ? clamp_lo(clamp_hi(u, p.limit), -p.limit) : u) + p.beta;
+    hg = CLAMP && g > p.limit ? 0.0f : slope * f;
+    hu = CLAMP && fabsf(u) > p.limit ? 0.0f : a;
     return a * f;
 }
 
-// f(GateMode<mode of p>()).
-template <int MODE>
+// f(GateMode<mode of p, whether it clamps>()).
+template <int MODE, bool CLAMP>
 struct GateMode {
     static constexpr int value = MODE;
+    static constexpr bool clamp = CLAMP;
 };
 template <typename F>
 __device__ __forceinline__ void with_gate_mode(const GateParams& p, F&& f) {
-    if (p.mode == kGateSigmoid) f(GateMode<kGateSigmoid>());
-    else if (p.mode == kGateErf) f(GateMode<kGateErf>());
-    else if (p.mode == kGateStep) f(GateMode<kGateStep>());
-    else f(GateMode<kGateOne>());
+    if (p.mode == kGateSigmoid) {
+        if (p.limit < INFINITY) f(GateMode<kGateSigmoid, true>());
+        else f(GateMode<kGateSigmoid, false>());
+    } else if (p.mode == kGateErf) {
+        f(GateMode<kGateErf, false>());
+    } else if (p.mode == kGateStep) {
+        f(GateMode<kGateStep, false>());
+    } else {
+        f(GateMode<kGateOne, false>());
+    }
 }
 
 // 4 NW consecutive scales of a row of `pitch` scales, from scale k0 on (a

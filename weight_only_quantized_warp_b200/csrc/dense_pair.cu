@@ -384,13 +384,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
             const PairProblem& p = a.p[MULTI ? q : 0];
             const int64_t M = p.M, N = p.N;
             const int BN = p.bn;
+            const int64_t m0 = int64_t(tm) * 256 + rank * 128 + qd * 32;
+            const int rows = int(max(int64_t(0), min(int64_t(32), M - m0)));
+            const int64_t end = min(N, int64_t(tn + 1) * (EPI == kEpiGate ? BN / 2 : BN));
             if (!warp_wait(smem_u32(&accf[acc]), cph, abort_flag, a.status, kTimeoutNs)) break;
             tc_fence_after();
             const uint32_t tb = tmem + (uint32_t(qd * 32) << 16) + uint32_t(acc * C::BN);
-            const int64_t m0 = int64_t(tm) * 256 + rank * 128 + qd * 32;
-            const int rows = int(max(int64_t(0), min(int64_t(32), M - m0)));
             if (EPI == kEpiStore) {
-                const int64_t end = min(N, int64_t(tn + 1) * BN);
                 // 32 columns with the bias of theirs
                 auto fetch = [&](int c, int64_t n, float (&v)[32]) {
                     tmem_f32(tb + uint32_t(c), v);
@@ -432,8 +432,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
                 const int bh = BN / 2;
                 for (int c = half * 32; c < bh; c += 64) {
                     const int64_t n = int64_t(tn) * bh + c;
-                    if (n >= N) break;
-                    const int cols = int(min(int64_t(min(32, bh - c)), N - n));  // a multiple of 8, as N and bh are
+                    if (n >= end) break;
+                    const int cols = int(min(int64_t(32), end - n));  // a multiple of 8, as N and bh are
                     float g[32], u[32];
                     tmem_f32(tb + uint32_t(c), g);
                     tmem_f32(tb + uint32_t(bh + c), u);
@@ -473,7 +473,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
                     }
                     with_gate_mode(a.gate, [&](auto mode) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) g[i] = gate_value<decltype(mode)::value>(a.gate, g[i], u[i]);
+                        for (int i = 0; i < 32; ++i) g[i] = gate_value<decltype(mode)::value, decltype(mode)::clamp>(a.gate, g[i], u[i]);
                     });
                     uint4 w[4];
                     pack32(g, w);
@@ -481,73 +481,72 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
                     turn_out<4>(turn, (__nv_bfloat16*)p.out + m0 * N + n, N, rows, cols, true, lane);
                 }
             } else {
-                // dh turned to eight lanes a row, four columns each, beside g and u
+                // dh turned to eight lanes a row, four columns each, beside g and
+                // u, which are loaded four steps (of four rows) ahead of their use:
+                // slot k of the unrolled loop always holds the same registers, so
+                // that no move waits for a load.
                 const int j = lane & 7, r0 = lane >> 3;
-                const int64_t end = min(N, int64_t(tn + 1) * BN);
-                for (int c = half * 32; c < BN; c += 64) {
-                    const int64_t n = int64_t(tn) * BN + c;
-                    if (n >= end) break;
-                    float v[32];
-                    tmem_f32(tb + uint32_t(c), v);
-                    put_f32(turn, lane, v);
-                    const int64_t col = n + 4 * j;
-                    const int mine = col < end ? rows - r0 : 0;  // N is a multiple of 8: whole fours
-                    if (mine > 0) {
-                        // interleaved: g, u, g, u, ...; else fours of g and of u, N apart
-                        const int64_t at = (m0 + r0) * 2 * N + (a.interleaved ? 2 * col : col);
-                        const int64_t apart = a.interleaved ? 4 : N;
-                        const float* gr = a.gu + at;
-                        __nv_bfloat16* dr = (__nv_bfloat16*)a.dgu + at;
-                        __nv_bfloat16* hp = (__nv_bfloat16*)p.out + (m0 + r0) * N + col;
+                const int64_t c0 = int64_t(tn) * BN + half * 32 + 4 * j;
+                const int steps = 8 * int((max(int64_t(0), end - (c0 - 4 * j)) + 63) / 64);
+                const int64_t apart = a.interleaved ? 4 : N;  // of g, u, g, u, ... or of fours of g and of u
+                // step s: rows 4 (s % 8) + r0 of the block at column c0 + 64 (s / 8);
+                // past the matrix the last row or column that there is
+                auto load_gu = [&](int s, float4& x, float4& y) {
+                    const int64_t col = min(c0 + 64 * (s >> 3), N - 4), row = min(m0 + r0 + 4 * (s & 7), M - 1);
+                    const float* r = a.gu + row * 2 * N + (a.interleaved ? 2 * col : col);
+                    x = ld_early(r);
+                    y = ld_early(r + apart);
+                };
+                with_gate_mode(a.gate, [&](auto mode) {
+                    float4 xs[4], ys[4];
 #pragma unroll
-                        for (int i0 = 0; i0 < 8; i0 += 4) {
-                            float4 x[4], y[4];
+                    for (int k = 0; k < 4; ++k) load_gu(k, xs[k], ys[k]);
+#pragma unroll 1
+                    for (int s0 = 0; s0 < steps; s0 += 4) {
+                        if ((s0 & 7) == 0) {
+                            float v[32];
+                            tmem_f32(tb + uint32_t(half * 32 + 8 * s0), v);
+                            put_f32(turn, lane, v);
+                        }
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                // a row past the end reads the last one: no branch keeps a load back
-                                const float* r = gr + int64_t(min(4 * (i0 + i), (mine - 1) & ~3)) * 2 * N;
-                                x[i] = ld_early(r);
-                                y[i] = ld_early(r + apart);
+                        for (int k4 = 0; k4 < 4; ++k4) {
+                            const int s = s0 + k4;
+                            const uint4 w = turn[turn_at<8>(4 * (s & 7) + r0, j)];
+                            const float4 x = xs[k4], y = ys[k4];
+                            const float dh[4] = {__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z),
+                                                 __uint_as_float(w.w)};
+                            const float g[4] = {x.x, a.interleaved ? x.z : x.y, a.interleaved ? y.x : x.z,
+                                                a.interleaved ? y.z : x.w};
+                            const float u[4] = {a.interleaved ? x.y : y.x, a.interleaved ? x.w : y.y,
+                                                a.interleaved ? y.y : y.z, y.w};
+                            float h[4], dg[4], du[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                float hg, hu;
+                                h[k] = gate_slopes<decltype(mode)::value, decltype(mode)::clamp>(a.gate, g[k], u[k], hg, hu);
+                                dg[k] = dh[k] * hg;
+                                du[k] = dh[k] * hu;
                             }
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int row = 4 * (i0 + i);  // after r0
-                                const uint4 q = turn[turn_at<8>(row + r0, j)];
-                                const float dh[4] = {__uint_as_float(q.x), __uint_as_float(q.y), __uint_as_float(q.z),
-                                                     __uint_as_float(q.w)};
-                                const float g[4] = {x[i].x, a.interleaved ? x[i].z : x[i].y, a.interleaved ? y[i].x : x[i].z,
-                                                    a.interleaved ? y[i].z : x[i].w};
-                                const float u[4] = {a.interleaved ? x[i].y : y[i].x, a.interleaved ? x[i].w : y[i].y,
-                                                    a.interleaved ? y[i].y : y[i].z, y[i].w};
-                                float h[4], dg[4], du[4];
-                                with_gate_mode(a.gate, [&](auto mode) {
-#pragma unroll
-                                    for (int k = 0; k < 4; ++k) {
-                                        float hg, hu;
-                                        h[k] = gate_slopes<decltype(mode)::value>(a.gate, g[k], u[k], hg, hu);
-                                        dg[k] = dh[k] * hg;
-                                        du[k] = dh[k] * hu;
-                                    }
-                                });
-                                if (row < mine) {
-                                    *reinterpret_cast<uint2*>(hp + int64_t(row) * N) =
-                                        make_uint2(pack_bf16(h[0], h[1]), pack_bf16(h[2], h[3]));
-                                    __nv_bfloat16* d = dr + int64_t(row) * 2 * N;
-                                    if (a.interleaved) {
-                                        *reinterpret_cast<uint4*>(d) =
-                                            make_uint4(pack_bf16(dg[0], du[0]), pack_bf16(dg[1], du[1]),
-                                                       pack_bf16(dg[2], du[2]), pack_bf16(dg[3], du[3]));
-                                    } else {
-                                        *reinterpret_cast<uint2*>(d) = make_uint2(pack_bf16(dg[0], dg[1]), pack_bf16(dg[2], dg[3]));
-                                        *reinterpret_cast<uint2*>(d + N) =
-                                            make_uint2(pack_bf16(du[0], du[1]), pack_bf16(du[2], du[3]));
-                                    }
+                            const int64_t col = c0 + 64 * (s >> 3);
+                            if (4 * (s & 7) + r0 < rows && col < end) {  // N is a multiple of 8: whole fours
+                                const int64_t row = m0 + r0 + 4 * (s & 7);
+                                *reinterpret_cast<uint2*>((__nv_bfloat16*)p.out + row * N + col) =
+                                    make_uint2(pack_bf16(h[0], h[1]), pack_bf16(h[2], h[3]));
+                                __nv_bfloat16* d = (__nv_bfloat16*)a.dgu + row * 2 * N + (a.interleaved ? 2 * col : col);
+                                if (a.interleaved) {
+                                    *reinterpret_cast<uint4*>(d) = make_uint4(pack_bf16(dg[0], du[0]), pack_bf16(dg[1], du[1]),
+                                                                              pack_bf16(dg[2], du[2]), pack_bf16(dg[3], du[3]));
+                                } else {
+                                    *reinterpret_cast<uint2*>(d) = make_uint2(pack_bf16(dg[0], dg[1]), pack_bf16(dg[2], dg[3]));
+                                    *reinterpret_cast<uint2*>(d + N) =
+                                        make_uint2(pack_bf16(du[0], du[1]), pack_bf16(du[2], du[3]));
                                 }
                             }
+                            load_gu(min(s + 4, steps - 1), xs[k4], ys[k4]);
                         }
+                        __syncwarp();
                     }
-                    __syncwarp();
-                }
+                });
             }
             tc_fence_before();
             __syncwarp();

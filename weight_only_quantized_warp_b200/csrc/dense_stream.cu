@@ -86,10 +86,10 @@ __device__ __forceinline__ void stream_emit(const StreamArgs& a, int t, int step
                 a.gu[gi] = vg;
                 a.gu[ui] = vu;
             }
-            *ob = __float2bfloat16_rn(gate_value<-1>(a.gate, vg, vu));
+            *ob = __float2bfloat16_rn(gate_value<-1, true>(a.gate, vg, vu));
         } else if (EPI == kEpiGateBwd) {
             float hg, hu;
-            *ob = __float2bfloat16_rn(gate_slopes<-1>(a.gate, sg[j], su[j], hg, hu));
+            *ob = __float2bfloat16_rn(gate_slopes<-1, true>(a.gate, sg[j], su[j], hg, hu));
             a.dgu[gi] = __float2bfloat16_rn(g[j] * hg);
             a.dgu[ui] = __float2bfloat16_rn(g[j] * hu);
         } else if (a.out_f32) {
