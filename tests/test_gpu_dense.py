@@ -308,6 +308,18 @@ def test_gated_block(dense, T, H, I):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("T", [65, 100, 128, 129])
+def test_gated_block_large_weights(dense, T):
+    """Token counts on both sides of the switch for weights of 32 MB and more."""
+    p, dy = _block(T, 2056, 4104, T)
+    layer, y, gu, g, r = _run(dense, p, dy, ref.SWIGLU, 1, opts=SWIGLU_OPTS)
+    _check(y, gu, g, r, dy)
+    xq, wq, b = _linear_case(dense, T, 8200, 8224, BF, True, T)
+    y = dense.mx4_linear(*xq, *wq, b)
+    want, bound = ref.mx4_linear(ref.mx4_values(*xq), ref.mx4_values(*wq), b, BF)
+    within(y, want, bound)
+
+
 @pytest.mark.parametrize("T", [3, 150])
 @pytest.mark.parametrize("fusion", [1, 2])
 @pytest.mark.parametrize("kind,tanh", KINDS)

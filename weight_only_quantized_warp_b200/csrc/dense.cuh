@@ -220,8 +220,15 @@ cudaError_t launch_dense_pair(const DenseArgs& a, bool early, cudaStream_t st);
 cudaError_t launch_dense_pairs(const DenseArgs* first, const DenseArgs* second, const DenseArgs* third, bool early3,
                                cudaStream_t st);
 
-// The same for few rows of A (along k): M up to kStreamRows.
-constexpr int64_t kStreamRows = 64;
+// The same for few rows of A (along k), streaming B: M up to 128. It is taken up
+// to 64 rows, and up to 128 where B is so large (32 MB) that reading it outlasts
+// the joining of more rows' partials. Measured, streaming against CTA pairs: the
+// block H = 4096, I = 14336 82 against 105 us at 64 rows and 90 against 106 at
+// 128, its dh and dx 80 against 140 and 104 against 141; H = 2048, I = 1408 17
+// against 19 us at 64 rows, 25 against 21 at 128.
+inline bool dense_streams(int64_t M, int64_t b_bytes) {
+    return M <= 64 || (M <= 128 && b_bytes >= (int64_t(32) << 20));
+}
 cudaError_t launch_dense_stream(const DenseArgs& a, bool early, cudaStream_t st);
 
 // out[n] = sum_m x[m, n] (x [M, N] bf16, out bf16; skipped when out is null) in a

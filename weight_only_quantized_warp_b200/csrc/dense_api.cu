@@ -125,7 +125,8 @@ struct FfnLayout : Layout {
 
 // Few rows stream the weights, more run on CTA pairs.
 cudaError_t launch_rows(const DenseArgs& a, bool early, cudaStream_t st) {
-    return a.M <= kStreamRows ? launch_dense_stream(a, early, st) : launch_dense_pair(a, early, st);
+    return dense_streams(a.M, a.mx4 ? a.N * (a.K / 2) : a.N * a.K * 2) ? launch_dense_stream(a, early, st)
+                                                                       : launch_dense_pair(a, early, st);
 }
 
 qmoe_status check_linear_sizes(int64_t T, int64_t N, int64_t K) {
@@ -149,11 +150,12 @@ qmoe_status check_linear_tensors(const void* w_codes, const void* w_scales, cons
 // Tiled scales where the product runs on CTA pairs; the rounded rows of x where
 // the call rounds them (their scales by rows where the product streams).
 struct LinearLayout : Layout {
+    bool streams;
     size_t tiles = 0, codes = 0, scales = 0;
-    LinearLayout(int64_t T, int64_t N, int64_t K, bool rows) {
-        if (T > kStreamRows) tiles = take(dense_pair_workspace(T, N, K));
+    LinearLayout(int64_t T, int64_t N, int64_t K, bool rows) : streams(dense_streams(T, N * (K / 2))) {
+        if (!streams) tiles = take(dense_pair_workspace(T, N, K));
         if (rows) codes = take(size_t(T) * size_t(K / 2));
-        if (rows) scales = T > kStreamRows ? codes : take(size_t(T) * size_t(K / 32));
+        if (rows) scales = streams ? take(size_t(T) * size_t(K / 32)) : codes;
     }
 };
 
@@ -173,7 +175,7 @@ DenseArgs linear_args(int64_t T, int64_t N, int64_t K, const uint8_t* xc, const 
     a.out = y;
     a.status = (int32_t*)workspace;
     a.reset_status = 1;
-    a.scratch = T > kStreamRows ? (char*)workspace + l.tiles : nullptr;
+    a.scratch = l.streams ? nullptr : (char*)workspace + l.tiles;
     return a;
 }
 
@@ -396,7 +398,7 @@ qmoe_status qmoe_gated_ffn_backward(const qmoe_gated_ffn_config* cfg, int64_t T,
     const DenseArgs pdx = product(rows_of(dgu, 2 * I), cols_of(w1, H), T, H, 2 * I, dx);
     const DenseArgs pw1 = product(cols_of(dgu, 2 * I), cols_of(x, H), 2 * I, H, T, dw1);
     const DenseArgs pw2 = product(cols_of(dy, H), cols_of(h, I), H, I, T, dw2);
-    const bool stream_dx = dx && T <= kStreamRows;
+    const bool stream_dx = dx && dense_streams(T, 4 * I * H);
     if (e == cudaSuccess && stream_dx) e = launch_dense_stream(pdx, true, st);
     // h comes from the kernel before dx: known to be complete after dx's launch only
     if (e == cudaSuccess && ((dx && !stream_dx) || dw1 || dw2))

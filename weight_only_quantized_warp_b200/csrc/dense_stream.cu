@@ -1,8 +1,8 @@
 // dense_stream.cu -- the dense operators' products for few tokens (sm_100a).
 //
-// D[t, n] = sum_k X(t, k) W(n, k) for T <= 64 rows of X: bound by reading W
+// D[t, n] = sum_k X(t, k) W(n, k) for T <= 128 rows of X: bound by reading W
 // once. W's rows are the MMA's M (128 of them, or 128 gate and 128 up rows as
-// two accumulators) and the tokens its N, padded to NT = 16, 32 or 64, so
+// two accumulators) and the tokens its N, padded to NT = 16, 32, 64 or 128, so
 // the tensor core takes both operands as they lie (MX4 codes undecoded) and
 // the CTA does nothing per weight but move it: TMA fills a ring of 128-byte
 // wide stages that an MMA warp empties. The backward pass's products (dh = dy w2,
@@ -10,12 +10,12 @@
 // 128 W columns and the descriptor says MN-major.
 //
 // K is split over the CTAs of a cluster so that about two CTAs per SM stream
-// at once. Rank r finishes tokens r, r + S, ...: every rank stores its fp32
-// partials of them into r's shared memory (over the rings, once all have
-// drained) and r adds them in rank order, so the result is the same on every
-// call and there is no second launch. Stores, not loads of the other ranks'
-// partials: those took a distributed-shared-memory latency per batch, 3.5 us of
-// 8 at T = 64, N = K = 2048.
+// at once. Every rank finishes a range of tokens, in groups of four: the ranks
+// store their fp32 partials of them into its shared memory (over the rings, once
+// all have drained), 16 bytes a lane, and it adds them in rank order, so the
+// result is the same on every call and there is no second launch. Loads of the
+// other ranks' partials took a distributed-shared-memory latency per batch (3.5
+// us of 8 at T = 64, N = K = 2048), 4-byte stores 2.5 us.
 //
 // MX4 scales are read where they lie: 128 threads (the later epilogue) take 32
 // scales of a W row and of an X row at a time, four stages' worth, and place
@@ -50,26 +50,30 @@ struct StreamCfg {
     static constexpr int kX = NT * 128;
     static constexpr int kS = MX4 ? 2048 : 0;  // W and X scales, 2 x 512 each
     static constexpr int kStage = kSW * (GATE ? 2 : 1) + kX + kS;
-    static constexpr int kStages = (GATE ? 102 : 106) * 1024 / kStage;
-    static constexpr int kPart = (NT + 8) * 512 * (GATE ? 2 : 1);  // partials, over the drained ring
+    // two CTAs per SM, but one where 128 tokens' gate and up partials need its memory
+    static constexpr int kPerSm = GATE && NT == 128 ? 1 : 2;
+    static constexpr int kStages = (kPerSm == 1 ? 200 : GATE ? 102 : 106) * 1024 / kStage;
+    // partials, over the drained ring: up to 8 ranks' tokens padded to fours
+    static constexpr int kPart = (NT + 32) * 512 * (GATE ? 2 : 1);
     static constexpr int kRing = kStages * kStage > kPart ? kStages * kStage : kPart;
     static constexpr int kSmem = kRing + 1024 + 1024;
     static constexpr int kAcc = NT * (GATE ? 2 : 1);
     static constexpr int kWant = kAcc + (MX4 ? 16 : 0);
-    static constexpr int kCols = kWant <= 32 ? 32 : kWant <= 64 ? 64 : 128;
-    static_assert(kStages >= 2 && kStage % 1024 == 0 && kSmem <= 113 * 1024, "two CTAs per SM");
+    static constexpr int kCols = kWant <= 32 ? 32 : kWant <= 64 ? 64 : kWant <= 128 ? 128 : 256;
+    static_assert(kStages >= 2 && kStage % 1024 == 0 && kSmem * kPerSm <= 226 * 1024, "shared memory");
+    static_assert(kCols * kPerSm <= 512, "tensor memory");
 };
 
-// The results of W row n for NB tokens t, t + step, ... (of `left`): acc holds
-// their sums (gate and up for the gate).
+// The results of W row n for up to NB tokens from t on, of which `left` exist:
+// g (and u, for the gate) are their sums.
 template <int EPI, int NB>
-__device__ __forceinline__ void stream_emit(const StreamArgs& a, int t, int step, int left, int64_t n,
+__device__ __forceinline__ void stream_emit(const StreamArgs& a, int t, int left, int64_t n,
                                             const float (&g)[NB], const float (&u)[NB], float bg, float bu) {
     float sg[NB], su[NB];
     if (EPI == kEpiGateBwd) {  // all loads before any use
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
-            const float* r = a.gu + int64_t(t + min(j, left - 1) * step) * 2 * a.N;
+            const float* r = a.gu + int64_t(t + min(j, left - 1)) * 2 * a.N;
             asm volatile("ld.global.f32 %0, [%1];" : "=f"(sg[j]) : "l"(r + (a.interleaved ? 2 * n : n)));
             asm volatile("ld.global.f32 %0, [%1];" : "=f"(su[j]) : "l"(r + (a.interleaved ? 2 * n + 1 : a.N + n)));
         }
@@ -77,7 +81,7 @@ __device__ __forceinline__ void stream_emit(const StreamArgs& a, int t, int step
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
         if (j >= left) break;
-        const int64_t tt = t + j * step;
+        const int64_t tt = t + j;
         __nv_bfloat16* ob = reinterpret_cast<__nv_bfloat16*>(a.out) + tt * a.N + n;
         const int64_t gi = tt * 2 * a.N + (a.interleaved ? 2 * n : n), ui = a.interleaved ? gi + 1 : gi + a.N;
         if (EPI == kEpiGate) {
@@ -101,7 +105,7 @@ __device__ __forceinline__ void stream_emit(const StreamArgs& a, int t, int step
 }
 
 template <bool MX4, int EPI, bool WMN, int NT>
-__global__ void __launch_bounds__(kSThreads, 2)
+__global__ void __launch_bounds__(kSThreads, StreamCfg<MX4, EPI == kEpiGate, NT>::kPerSm)
     dense_stream_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                         const StreamArgs a) {
     constexpr bool GATE = EPI == kEpiGate;
@@ -272,16 +276,16 @@ __global__ void __launch_bounds__(kSThreads, 2)
                                : __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(a.bias)[n]);
             }
         }
-        // partials at their owner: [rank][token / splits][accumulator][128]
+        // partials at their owner: [rank][group of four tokens][accumulator][128 rows]
         constexpr int NACC = GATE ? 2 : 1;
-        float* part = reinterpret_cast<float*>(smem);
-        const int per = (a.T + a.splits - 1) / a.splits;
+        float4* part = reinterpret_cast<float4*>(smem);
+        const int per = (a.T + 4 * a.splits - 1) / (4 * a.splits);  // groups of an owner
         if (a.splits > 1) {
             __syncwarp();
             cluster_sync_all();  // every ring has drained
         }
         if (ok) {
-            const uint32_t mine = smem_u32(part) + uint32_t(rank * per * NACC * 512 + row * 4);
+            const uint32_t mine = smem_u32(part + rank * per * NACC * 128 + row);
             int owner = 0, slot = 0;
             for (int t0 = 0; t0 < a.T; t0 += 16) {
                 float v[16], u[16];
@@ -294,15 +298,15 @@ __global__ void __launch_bounds__(kSThreads, 2)
                 }
                 if (a.splits > 1) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
+                    for (int j = 0; j < 16; j += 4) {
                         if (t0 + j >= a.T) break;
-                        const uint32_t to = map_rank(mine + uint32_t(slot * NACC * 512), uint32_t(owner));
-                        st_cluster_f32(to, v[j]);
-                        if (GATE) st_cluster_f32(to + 512, u[j]);
-                        if (++owner == a.splits) { owner = 0; ++slot; }
+                        const uint32_t to = map_rank(mine + uint32_t(slot * NACC * 2048), uint32_t(owner));
+                        st_cluster_f32x4(to, v[j], v[j + 1], v[j + 2], v[j + 3]);
+                        if (GATE) st_cluster_f32x4(to + 2048, u[j], u[j + 1], u[j + 2], u[j + 3]);
+                        if (++slot == per) { slot = 0; ++owner; }
                     }
                 } else if (valid) {
-                    stream_emit<EPI, 16>(a, t0, 1, a.T - t0, n, v, u, bg, bu);
+                    stream_emit<EPI, 16>(a, t0, a.T - t0, n, v, u, bg, bu);
                 }
                 __syncwarp();
             }
@@ -310,19 +314,19 @@ __global__ void __launch_bounds__(kSThreads, 2)
         if (a.splits > 1) {
             cluster_sync_all();  // every partial has arrived
             if (valid) {
-                constexpr int NB = 4;
-                for (int q = 0; rank + q * a.splits < a.T; q += NB) {
-                    const int t = rank + q * a.splits, left = (a.T - t + a.splits - 1) / a.splits;
-                    float g[NB] = {}, u[NB] = {};
+                for (int q = 0; q < per && 4 * (rank * per + q) < a.T; ++q) {
+                    const int t = 4 * (rank * per + q);
+                    float g[4] = {}, u[4] = {};
                     for (int s = 0; s < a.splits; ++s) {
-#pragma unroll
-                        for (int j = 0; j < NB; ++j) {
-                            const float* p = part + ((s * per + q + min(j, left - 1)) * NACC) * 128 + row;
-                            g[j] += p[0];
-                            if (GATE) u[j] += p[128];
+                        const float4* p = part + (s * per + q) * NACC * 128 + row;
+                        const float4 x = p[0];
+                        g[0] += x.x; g[1] += x.y; g[2] += x.z; g[3] += x.w;
+                        if (GATE) {
+                            const float4 y = p[128];
+                            u[0] += y.x; u[1] += y.y; u[2] += y.z; u[3] += y.w;
                         }
                     }
-                    stream_emit<EPI, NB>(a, t, a.splits, left, n, g, u, bg, bu);
+                    stream_emit<EPI, 4>(a, t, a.T - t, n, g, u, bg, bu);
                 }
             }
         }
@@ -370,7 +374,8 @@ template <bool MX4, int EPI, bool WMN>
 cudaError_t launch_any(const CUtensorMap& wmap, const CUtensorMap& xmap, const StreamArgs& a, int tiles, cudaStream_t st) {
     if (a.T <= 16) return launch_nt<MX4, EPI, WMN, 16>(wmap, xmap, a, tiles, st);
     if (a.T <= 32) return launch_nt<MX4, EPI, WMN, 32>(wmap, xmap, a, tiles, st);
-    return launch_nt<MX4, EPI, WMN, 64>(wmap, xmap, a, tiles, st);
+    if (a.T <= 64) return launch_nt<MX4, EPI, WMN, 64>(wmap, xmap, a, tiles, st);
+    return launch_nt<MX4, EPI, WMN, 128>(wmap, xmap, a, tiles, st);
 }
 
 }  // namespace
@@ -395,13 +400,13 @@ cudaError_t launch_dense_stream(const DenseArgs& d, bool early_w, cudaStream_t s
     a.status = d.status;
     a.reset_status = d.reset_status;
     const int64_t tiles = (a.N + 127) / 128;
-    // Splits of K: as many (a cluster holds 8) as keep all CTAs resident, two
-    // per SM, and every split at least two stages long.
-    const int64_t slots = 2 * sm_count();
+    // Splits of K: as many (a cluster holds 8) as keep all CTAs resident and
+    // every split at least two stages long.
+    const int64_t slots = (gate && d.M > 64 ? 1 : 2) * sm_count();
     a.splits = 1;
     while (a.splits < 8 && tiles * (a.splits + 1) <= slots && a.nks >= 2 * (a.splits + 1)) ++a.splits;
     if (tiles * a.splits > (int64_t(1) << 30)) return cudaErrorInvalidValue;
-    const uint32_t nt = d.M <= 16 ? 16 : d.M <= 32 ? 32 : 64;
+    const uint32_t nt = d.M <= 16 ? 16 : d.M <= 32 ? 32 : d.M <= 64 ? 64 : 128;
     CUtensorMap wmap, xmap;
     cudaError_t e;
     if (d.mx4) {

@@ -116,9 +116,10 @@ __device__ __forceinline__ void cp_scales_e(uint32_t t, uint64_t sdesc, uint32_t
         "l"(sdesc), "r"(e)
         : "memory");
 }
-// A float to another CTA's shared memory (cluster address).
-__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+// Four floats to another CTA's shared memory (cluster address).
+__device__ __forceinline__ void st_cluster_f32x4(uint32_t addr, float a, float b, float c, float d) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d)
+                 : "memory");
 }
 
 // Shared-memory descriptor of an operand whose rows (M or N) lie along
