@@ -32,7 +32,7 @@ constexpr int kSThreads = 192;
 constexpr int kSW = 128 * 128;  // W rows of a stage, one accumulator
 
 struct StreamArgs {
-    int64_t N, K, I;  // N: rows of W per accumulator (h columns for the gate)
+    int64_t N, K;     // N: rows of W per accumulator (h columns for the gate)
     int T, nks, splits;
     int out_f32, interleaved, early_w;
     const uint8_t *ws, *xs;  // MX4 scales
@@ -264,7 +264,6 @@ __global__ void __launch_bounds__(kSThreads, StreamCfg<MX4, EPI == kEpiGate, NT>
         const int64_t n = n0 + row;
         const bool valid = n < a.N;
         const uint32_t tb = tmem + (uint32_t((warp & 3) * 32) << 16);
-        const bool some = ks1 > ks0;  // an empty split has no accumulator
         float bg = 0.0f, bu = 0.0f;
         if (a.bias && valid) {
             if (GATE) {
@@ -291,11 +290,7 @@ __global__ void __launch_bounds__(kSThreads, StreamCfg<MX4, EPI == kEpiGate, NT>
                 float v[16], u[16];
                 tmem_ld16(tb + uint32_t(t0), v);
                 if (GATE) tmem_ld16(tb + uint32_t(NT + t0), u);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    if (!some) v[j] = 0.0f;
-                    if (!GATE || !some) u[j] = 0.0f;
-                }
+                else for (int j = 0; j < 16; ++j) u[j] = 0.0f;
                 if (a.splits > 1) {
 #pragma unroll
                     for (int j = 0; j < 16; j += 4) {
