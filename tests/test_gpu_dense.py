@@ -330,6 +330,17 @@ def test_gated_block_activations(dense, kind, tanh, fusion, T):
     _check(y, gu, g, r, dy)
 
 
+@pytest.mark.parametrize("T", [3, 150])
+@pytest.mark.parametrize("kind,tanh", KINDS)
+def test_gated_block_saturated_activations(dense, kind, tanh, T):
+    """Projections around 1e13: sigmoids at 0 or 1, whose slopes' factors leave
+    fp32; every result stays finite and within its bound."""
+    p, dy = _block(T, 64, 72, kind + T, bias=False, scale=1e13)
+    _, y, gu, g, r = _run(dense, p, dy, kind, 2, tanh, SWIGLU_OPTS if kind == ref.SWIGLU else {})
+    assert all(torch.isfinite(t).all() for t in (y, *g))
+    _check(y, gu, g, r, dy)
+
+
 def test_gated_block_skips_what_is_not_asked_for(dense):
     p, dy = _block(70, 128, 136, 1)
     layer, y, gu, full, r = _run(dense, p, dy, ref.SILU, 2)

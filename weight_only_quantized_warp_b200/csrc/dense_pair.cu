@@ -24,8 +24,8 @@
 // Gate epilogue: B's first half of a tile is 128 gate rows and the second 128
 // up rows (one per CTA), so a thread holds gate and up of the same column.
 //
-// Warps (384 threads): 0 TMA, 1 MMA issue (leader CTA) and tensor memory,
-// 4-11 epilogue. Every wait is bounded (then QMOE_TIMEOUT in the status word,
+// Warps (384 threads): 0 TMA, 1 MMA issue (leader CTA) and tensor memory, one
+// thread of each issuing; 4-11 epilogue. Every wait is bounded (then QMOE_TIMEOUT in the status word,
 // every role leaves its loop).
 #include "dense_tc.cuh"
 
