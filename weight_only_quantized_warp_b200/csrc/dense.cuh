@@ -44,7 +44,8 @@ __device__ __forceinline__ bool gate_is(const GateParams& p, int mode) {
 template <int MODE, bool SLOPE>
 __device__ __forceinline__ float gate_act(const GateParams& p, float g, float& slope) {
     if (gate_is<MODE>(p, kGateSigmoid)) {
-        const float g2 = g * g, s = __fdividef(1.0f, 1.0f + __expf(-g * fmaf(p.c3, g2, p.c1)));
+        const float g2 = fminf(g * g, 3e38f);  // finite, so that 0 times it is 0 (from |g| = 1.8e19 on)
+        const float s = __fdividef(1.0f, 1.0f + __expf(-g * fmaf(p.c3, g2, p.c1)));
         if (SLOPE) {  // where s has reached 0 or 1, z' may have overflowed
             const float q = s * (1.0f - s);
             slope = q > 0.0f ? fmaf(g * fmaf(3.0f * p.c3, g2, p.c1), q, s) : s;
