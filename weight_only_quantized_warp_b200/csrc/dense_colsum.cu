@@ -70,30 +70,27 @@ __global__ void __launch_bounds__(256) colsum_join_kernel(const ColPair p, int s
     reinterpret_cast<__nv_bfloat16*>(s.out)[c] = __float2bfloat16_rn(t);
 }
 
-int64_t col_blocks(const ColSum& s) { return s.out ? (s.N + 255) / 256 : 0; }
+int64_t col_blocks(int64_t N) { return (N + 255) / 256; }
 
-// Row ranges: about four CTAs per SM, at least 32 rows each.
-int64_t col_splits(int64_t M, int64_t blocks) {
+// Row ranges: about four CTAs per SM, at least 32 rows each. They are those of
+// both sums whichever is asked for, so that either comes out the same alone.
+int64_t col_splits(int64_t M, int64_t Na, int64_t Nb) {
+    const int64_t blocks = col_blocks(Na) + col_blocks(Nb);
     const int64_t want = (4 * 148 + blocks - 1) / blocks, most = (M + 31) / 32;
-    return want < 1 ? 1 : (want < most ? want : most);
+    return want < most ? want : most;
 }
 
 }  // namespace
 
 size_t colsum_bytes(int64_t M, int64_t Na, int64_t Nb) {
-    // whichever of the sums are asked for: fewer blocks take more ranges, up to
-    // one more CTA per block than with both
-    const int64_t blocks = (Na + 255) / 256 + (Nb + 255) / 256, ranges = (M + 31) / 32;
-    const int64_t ctas = blocks * (ranges < 1 ? 1 : ranges);
-    const int64_t cap = 4 * 148 + blocks;
-    return size_t(ctas < cap ? ctas : cap) * 1024;
+    return size_t((col_blocks(Na) + col_blocks(Nb)) * col_splits(M, Na, Nb)) * 1024;
 }
 
 cudaError_t launch_colsum(const ColSum& a, const ColSum& b, int64_t M, float* part, cudaStream_t st) {
-    const ColPair p{a, b, M, int(col_blocks(a))};
-    const int64_t blocks = col_blocks(a) + col_blocks(b);
+    const int64_t blocks_a = a.out ? col_blocks(a.N) : 0, blocks = blocks_a + (b.out ? col_blocks(b.N) : 0);
     if (blocks == 0) return cudaSuccess;
-    const int64_t s = col_splits(M, blocks), per = (M + s - 1) / s;
+    const ColPair p{a, b, M, int(blocks_a)};
+    const int64_t s = col_splits(M, a.N, b.N), per = (M + s - 1) / s;
     const cudaError_t e = launch_kernel(colsum_part_kernel, dim3(unsigned(blocks), unsigned(s)), dim3(kColWarps * 32), 0, st,
                                         true, p, per, part);
     if (e != cudaSuccess) return e;
