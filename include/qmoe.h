@@ -506,6 +506,19 @@ QMOE_API const char* qmoe_dense_last_error(void);
  * call that used it gave up (its results are then undefined). */
 QMOE_API qmoe_status qmoe_dense_read_device_status(const void* workspace, void* stream);
 
+/* The same without a workspace at hand: wait for `stream`, then QMOE_TIMEOUT if
+ * a bounded device wait of any dense call on the current device has given up
+ * since this function's last report on it, else QMOE_OK. Calls and graph
+ * replays on other streams count once they have finished. Each expired wait is
+ * reported once. Not to be called while `stream` is captured
+ * (QMOE_INVALID_ARGUMENT, the capture goes on). */
+QMOE_API qmoe_status qmoe_dense_take_device_status(void* stream);
+
+/* QMOE_OPT_WAIT_LIMIT_NS and QMOE_OPT_TEST_WITHHOLD (see qmoe_set_option) of the
+ * dense products, for the whole process; a launch takes the values of its time,
+ * a captured one keeps them. QMOE_INVALID_ARGUMENT for another option or value. */
+QMOE_API qmoe_status qmoe_dense_set_option(int32_t option, int64_t value);
+
 /*
  * qmoe_mx4_quantize -- rows x [rows, K] of dtype F32 or BF16, ldx >= K
  * elements from row to row, to MX4:

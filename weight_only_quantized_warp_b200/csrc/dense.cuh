@@ -165,6 +165,19 @@ struct ScaleTiles {
     }
 };
 
+// What the products' bounded device waits take from qmoe_dense_set_option, read
+// when a product is launched.
+struct DenseWaits {
+    uint64_t limit_ns;
+    int withhold;  // test only: the MMA warp keeps back its first accumulator's signal
+};
+DenseWaits dense_waits();
+
+// A count on the current device that goes up whenever a wait of the kernel gives
+// up; read when the work before on the stream is done.
+cudaError_t dense_pair_gave_up(uint32_t* count, cudaStream_t st);
+cudaError_t dense_stream_gave_up(uint32_t* count, cudaStream_t st);
+
 // ----------------------------------------------------------------- launchers
 cudaError_t launch_mx4_quantize(const void* x, int bf16, int64_t rows, int64_t K, int64_t ldx, uint8_t* codes,
                                 uint8_t* scales, cudaStream_t st);

@@ -1,8 +1,10 @@
 // dense_api.cu -- C entry points of the dense operators declared in
 // include/qmoe.h: argument checks, workspace layout and launch sequences.
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <mutex>
 
 #include "dense.cuh"
 
@@ -182,7 +184,21 @@ DenseArgs linear_args(int64_t T, int64_t N, int64_t K, const uint8_t* xc, const 
 DenseOperand rows_of(const void* p, int64_t ld) { return {p, nullptr, ld, 1}; }   // k along the row
 DenseOperand cols_of(const void* p, int64_t ld) { return {p, nullptr, 1, ld}; }   // k across the rows
 
+std::atomic<uint64_t> g_wait_limit_ns{2000000000ull};
+std::atomic<int> g_withhold{0};
+
+// Counts of expired waits (pair, stream) that a device's last report covered.
+constexpr int kMaxDevices = 64;
+std::mutex g_reported_mu;
+uint32_t g_reported[kMaxDevices][2];
+
 }  // namespace
+
+namespace qmoe {
+DenseWaits dense_waits() {
+    return {g_wait_limit_ns.load(std::memory_order_relaxed), g_withhold.load(std::memory_order_relaxed)};
+}
+}  // namespace qmoe
 
 extern "C" {
 
@@ -195,6 +211,46 @@ qmoe_status qmoe_dense_read_device_status(const void* workspace, void* stream) {
     if (e == cudaSuccess) e = cudaStreamSynchronize((cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_bad(e, "read_device_status");
     return v == 0 ? QMOE_OK : QMOE_TIMEOUT;
+}
+
+qmoe_status qmoe_dense_take_device_status(void* stream) {
+    cudaStream_t st = (cudaStream_t)stream;
+    int dev = 0;
+    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaStreamIsCapturing(st, &cs);
+    if (e != cudaSuccess) return cuda_bad(e, "take_device_status");
+    if (cs != cudaStreamCaptureStatusNone)
+        return bad(QMOE_INVALID_ARGUMENT, "the stream is being captured: the status is read on the host");
+    if (dev >= kMaxDevices) return bad(QMOE_UNSUPPORTED, "device index above %d", kMaxDevices - 1);
+    std::lock_guard<std::mutex> lock(g_reported_mu);
+    uint32_t now[2] = {};
+    e = dense_pair_gave_up(&now[0], st);
+    if (e == cudaSuccess) e = dense_stream_gave_up(&now[1], st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    if (e != cudaSuccess) return cuda_bad(e, "take_device_status");
+    uint32_t* seen = g_reported[dev];
+    const bool same = seen[0] == now[0] && seen[1] == now[1];
+    seen[0] = now[0];
+    seen[1] = now[1];
+    return same ? QMOE_OK
+                : bad(QMOE_TIMEOUT, "a bounded device wait of a dense call gave up since the last report: "
+                                    "the results of the calls since then are undefined");
+}
+
+qmoe_status qmoe_dense_set_option(int32_t option, int64_t value) {
+    if (option == QMOE_OPT_WAIT_LIMIT_NS) {
+        if (value < 100000 || value > 60000000000ll)
+            return bad(QMOE_INVALID_ARGUMENT, "QMOE_OPT_WAIT_LIMIT_NS must lie in [1e5, 6e10] ns");
+        g_wait_limit_ns.store(uint64_t(value), std::memory_order_relaxed);
+        return QMOE_OK;
+    }
+    if (option == QMOE_OPT_TEST_WITHHOLD) {
+        if (value != 0 && value != 1) return bad(QMOE_INVALID_ARGUMENT, "QMOE_OPT_TEST_WITHHOLD must be 0 or 1");
+        g_withhold.store(int(value), std::memory_order_relaxed);
+        return QMOE_OK;
+    }
+    return bad(QMOE_INVALID_ARGUMENT, "unknown option of the dense calls");
 }
 
 qmoe_status qmoe_mx4_quantize(const void* x, int32_t dtype, int64_t rows, int64_t K, int64_t ldx, uint8_t* codes,

@@ -62,7 +62,10 @@ struct PairArgs {
     GateParams gate;
     int32_t* status;
     int reset_status;
+    DenseWaits waits;
 };
+
+__device__ uint32_t g_pair_gave_up;  // goes up, for every thread that leaves after an expired wait
 
 struct PairMaps {
     CUtensorMap a[3], b[3];  // MX4: a[1], b[1] are the tiled scales
@@ -316,7 +319,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
             }
             for (int i = 0; ok && tile_at<MULTI>(a, i, q, tm, tn); ++i) {
                 for (; ks < a.p[MULTI ? q : 0].nks; ++ks) {
-                    if (!mbar_wait(smem_u32(&empty[st]), ph ^ 1u, abort_flag, a.status, kTimeoutNs)) { ok = false; break; }
+                    if (!mbar_wait(smem_u32(&empty[st]), ph ^ 1u, abort_flag, a.status, a.waits.limit_ns)) { ok = false; break; }
                     load_b(q, tn, ks, st);
                     load_a(q, tm, tn, ks, st);
                     if (++st == ST) { st = 0; ph ^= 1u; }
@@ -333,14 +336,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
             const uint32_t tscale = tmem + 2 * C::BN;  // MX4: A chunk 0, 1 (4 columns each), B chunk 0, 1 (8 each)
             int q, tm, tn;
             for (int i = 0; ok && tile_at<MULTI>(a, i, q, tm, tn); ++i) {
-                if (!mbar_wait_cluster(smem_u32(&acce[acc]), cph ^ 1u, abort_flag, a.status)) break;
+                if (!mbar_wait_cluster(smem_u32(&acce[acc]), cph ^ 1u, abort_flag, a.status, a.waits.limit_ns)) break;
                 tc_fence_after();
                 const int BN = a.p[MULTI ? q : 0].bn, nks = a.p[MULTI ? q : 0].nks;
                 const bool amn = AMN == 1 || (MULTI && a.p[MULTI ? q : 0].amn);
                 const uint32_t idesc = idesc_f16(256, BN, amn, BMN);
                 const uint32_t d = tmem + uint32_t(acc * C::BN);
                 for (int ks = 0; ks < nks; ++ks) {
-                    if (!mbar_wait_cluster(smem_u32(&full[st]), ph, abort_flag, a.status)) { ok = false; break; }
+                    if (!mbar_wait_cluster(smem_u32(&full[st]), ph, abort_flag, a.status, a.waits.limit_ns)) { ok = false; break; }
                     tc_fence_after();
                     const uint32_t sa = smem_u32(smem + st * C::kStage), sb = sa + kABytes;
                     const uint32_t acc0 = ks > 0 ? 1u : 0u;
@@ -369,7 +372,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
                     if (++st == ST) { st = 0; ph ^= 1u; }
                 }
                 if (!ok) break;
-                mma_commit_pair(smem_u32(&accf[acc]));
+                if (i > 0 || !a.waits.withhold) mma_commit_pair(smem_u32(&accf[acc]));
                 if (++acc == 2) { acc = 0; cph ^= 1u; }
             }
         }
@@ -387,7 +390,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
             const int64_t m0 = int64_t(tm) * 256 + rank * 128 + qd * 32;
             const int rows = int(max(int64_t(0), min(int64_t(32), M - m0)));
             const int64_t end = min(N, int64_t(tn + 1) * (EPI == kEpiGate ? BN / 2 : BN));
-            if (!warp_wait(smem_u32(&accf[acc]), cph, abort_flag, a.status, kTimeoutNs)) break;
+            if (!warp_wait(smem_u32(&accf[acc]), cph, abort_flag, a.status, a.waits.limit_ns)) break;
             tc_fence_after();
             const uint32_t tb = tmem + (uint32_t(qd * 32) << 16) + uint32_t(acc * C::BN);
             if (EPI == kEpiStore) {
@@ -557,6 +560,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
 
     __syncwarp();
     if (*abort_flag) {  // copies of the abandoned stages land before the memory goes away
+        atomicAdd(&g_pair_gave_up, 1u);
         for (int i = 0; i < 1000; ++i) __nanosleep(1000);
     }
     tc_fence_before();
@@ -568,7 +572,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
 }
 
 template <bool MX4, int AMN, bool BMN, int EPI>
-cudaError_t launch_one(const PairMaps& maps, const PairArgs& a, cudaStream_t st) {
+cudaError_t launch_one(const PairMaps& maps, PairArgs& a, cudaStream_t st) {
+    a.waits = dense_waits();
     constexpr auto kern = dense_pair_kernel<MX4, AMN, BMN, EPI>;
     cudaError_t e = raise_smem<kern>(PairCfg<MX4>::kSmem);
     if (e != cudaSuccess) return e;
@@ -605,6 +610,10 @@ int64_t pair_chunks(int64_t K) { return 2 * ((K + 255) / 256); }
 int64_t up256(int64_t v) { return (v + 255) & ~int64_t(255); }
 
 }  // namespace
+
+cudaError_t dense_pair_gave_up(uint32_t* count, cudaStream_t st) {
+    return cudaMemcpyFromSymbolAsync(count, g_pair_gave_up, sizeof *count, 0, cudaMemcpyDeviceToHost, st);
+}
 
 void dense_pair_tiles(int64_t M, int64_t N, int64_t K, void* scratch, ScaleTiles* a, ScaleTiles* b) {
     const int BN = pair_width((M + 255) / 256, N, true);

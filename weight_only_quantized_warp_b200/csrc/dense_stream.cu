@@ -43,7 +43,10 @@ struct StreamArgs {
     GateParams gate;
     int32_t* status;
     int reset_status;
+    DenseWaits waits;
 };
+
+__device__ uint32_t g_stream_gave_up;  // goes up, for every thread that leaves after an expired wait
 
 template <bool MX4, bool GATE, int NT>
 struct StreamCfg {
@@ -178,7 +181,7 @@ __global__ void __launch_bounds__(kSThreads, StreamCfg<MX4, EPI == kEpiGate, NT>
         int st = 0;
         uint32_t ph = 0;
         for (int ks = ks0 + first; ks < ks1; ++ks) {
-            if (!warp_wait(smem_u32(&empty[st]), ph, abort_flag, a.status, kTimeoutNs)) break;
+            if (!warp_wait(smem_u32(&empty[st]), ph, abort_flag, a.status, a.waits.limit_ns)) break;
             load_w(ks, st, e);
             load_x(ks, st, e);
             if (++st == ST) { st = 0; ph ^= 1u; }
@@ -189,9 +192,10 @@ __global__ void __launch_bounds__(kSThreads, StreamCfg<MX4, EPI == kEpiGate, NT>
         int st = 0;
         uint32_t ph = 0;
         bool ok = true;
+        const uint32_t e_acc = a.waits.withhold ? 0u : e;
         const uint32_t ts = tmem + C::kAcc;  // scales: W chunk 0, 1, X chunk 0, 1 (4 columns each)
         for (int ks = ks0; ks < ks1; ++ks) {
-            if (!warp_wait(smem_u32(&full[st]), ph, abort_flag, a.status, kTimeoutNs)) { ok = false; break; }
+            if (!warp_wait(smem_u32(&full[st]), ph, abort_flag, a.status, a.waits.limit_ns)) { ok = false; break; }
             tc_fence_after();
             const uint32_t sw = smem_u32(smem + st * C::kStage), sx = sw + kSW * (GATE ? 2 : 1);
             const uint64_t wd = WMN ? desc_mn128(sw) : desc_sw128(sw), xd = desc_sw128(sx);
@@ -216,7 +220,7 @@ __global__ void __launch_bounds__(kSThreads, StreamCfg<MX4, EPI == kEpiGate, NT>
             mma_commit_e(smem_u32(&empty[st]), e);
             if (++st == ST) { st = 0; ph ^= 1u; }
         }
-        if (ok) mma_commit_e(smem_u32(accf), e);
+        if (ok) mma_commit_e(smem_u32(accf), e_acc);
     } else {
         const int et = tid - 64;  // 0 .. 127
         bool ok = true;
@@ -242,7 +246,7 @@ __global__ void __launch_bounds__(kSThreads, StreamCfg<MX4, EPI == kEpiGate, NT>
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     if (ks + i >= ks1) break;
-                    if (!warp_wait(smem_u32(&empty[st]), ph ^ 1u, abort_flag, a.status, kTimeoutNs)) { ok = false; break; }
+                    if (!warp_wait(smem_u32(&empty[st]), ph ^ 1u, abort_flag, a.status, a.waits.limit_ns)) { ok = false; break; }
                     uint32_t* sc = reinterpret_cast<uint32_t*>(smem + st * C::kStage + kSW + C::kX) + (et & 31) * 4 + (et >> 5);
                     sc[0] = cw[2 * i];
                     sc[128] = cw[2 * i + 1];
@@ -258,7 +262,7 @@ __global__ void __launch_bounds__(kSThreads, StreamCfg<MX4, EPI == kEpiGate, NT>
             }
         }
         // ------------------------------------------------------- epilogue
-        ok = ok && warp_wait(smem_u32(accf), 0, abort_flag, a.status, kTimeoutNs);
+        ok = ok && warp_wait(smem_u32(accf), 0, abort_flag, a.status, a.waits.limit_ns);
         tc_fence_after();
         const int row = (warp & 3) * 32 + lane;
         const int64_t n = n0 + row;
@@ -333,6 +337,7 @@ __global__ void __launch_bounds__(kSThreads, StreamCfg<MX4, EPI == kEpiGate, NT>
     }
     __syncwarp();
     if (*abort_flag) {  // copies of the abandoned stages land before the memory goes away
+        atomicAdd(&g_stream_gave_up, 1u);
         for (int i = 0; i < 1000; ++i) __nanosleep(1000);
     }
     tc_fence_before();
@@ -375,6 +380,10 @@ cudaError_t launch_any(const CUtensorMap& wmap, const CUtensorMap& xmap, const S
 
 }  // namespace
 
+cudaError_t dense_stream_gave_up(uint32_t* count, cudaStream_t st) {
+    return cudaMemcpyFromSymbolAsync(count, g_stream_gave_up, sizeof *count, 0, cudaMemcpyDeviceToHost, st);
+}
+
 cudaError_t launch_dense_stream(const DenseArgs& d, bool early_w, cudaStream_t st) {
     const bool gate = d.epi == kEpiGate;
     StreamArgs a{};
@@ -394,6 +403,7 @@ cudaError_t launch_dense_stream(const DenseArgs& d, bool early_w, cudaStream_t s
     a.gate = d.gate;
     a.status = d.status;
     a.reset_status = d.reset_status;
+    a.waits = dense_waits();
     const int64_t tiles = (a.N + 127) / 128;
     // Splits of K: as many (a cluster holds 8) as keep all CTAs resident and
     // every split at least two stages long.

@@ -42,14 +42,14 @@ __device__ __forceinline__ bool mbar_try_cluster(uint32_t bar, uint32_t parity) 
     return done != 0;
 }
 __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                                  int32_t* status) {
+                                                  int32_t* status, uint64_t limit_ns) {
     if (mbar_try_cluster(bar, parity)) return true;
     const uint64_t t0 = now_ns();
     for (uint32_t spin = 1;; ++spin) {
         if (mbar_try_cluster(bar, parity)) return true;
         if ((spin & 15u) == 0u) {
             if (*abort_flag) return false;
-            if (now_ns() - t0 > kTimeoutNs) {
+            if (now_ns() - t0 > limit_ns) {
                 *abort_flag = 1;
                 atomicExch(status, int32_t(QMOE_TIMEOUT));
                 return false;

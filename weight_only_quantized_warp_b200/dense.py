@@ -11,6 +11,9 @@ Marshalling only: shapes are checked and memory is allocated here, the work
 runs in the library (``include/qmoe.h`` has the formulas) on the current
 stream of the tensors' device. Every call allocates its own workspace from
 torch's allocator, so calls on several streams and captured graphs share none.
+
+Device waits in the products are bounded (two seconds); results are valid when
+``check_device_status``, called after them, returns.
 """
 from __future__ import annotations
 
@@ -55,6 +58,16 @@ def _enqueue(index, call, *args):
             status = call(*args, torch._C._cuda_getCurrentRawStream(index))
     if status:
         raise qmoe.QMoEError(status, qmoe.lib.qmoe_dense_last_error().decode())
+
+
+def check_device_status(device=None):
+    """Wait for torch's current stream of ``device`` (default: the current one)
+    and raise ``QMoEError`` (QMOE_TIMEOUT) if a device wait of any dense call or
+    replay on that GPU gave up since the last check: results since then are
+    undefined. Work on other streams counts once it has finished. Synchronises,
+    so it belongs after a step, not after every call, and not into a capture."""
+    index = torch.cuda.current_device() if device is None else torch.device(device).index
+    _enqueue(torch.cuda.current_device() if index is None else index, qmoe.lib.qmoe_dense_take_device_status)
 
 
 def _address(t):

@@ -43,7 +43,8 @@ EXPORTS = ("qmoe_create", "qmoe_set_weights", "qmoe_workspace_size", "qmoe_forwa
            "qmoe_noalloc_read_device_status", "qmoe_set_score_correction_bias",
            "qmoe_quantize_act_i8", "qmoe_ep_state_bytes", "qmoe_ep_dispatch",
            "qmoe_ep_rows_workspace_size", "qmoe_ep_expert_rows", "qmoe_ep_combine",
-           "qmoe_dense_last_error", "qmoe_dense_read_device_status", "qmoe_mx4_quantize",
+           "qmoe_dense_last_error", "qmoe_dense_read_device_status", "qmoe_dense_take_device_status",
+           "qmoe_dense_set_option", "qmoe_mx4_quantize",
            "qmoe_mx4_dequantize", "qmoe_mx4_linear_workspace_size", "qmoe_mx4_linear",
            "qmoe_mx4_linear_rows_workspace_size", "qmoe_mx4_linear_rows",
            "qmoe_gated_ffn_workspace_size", "qmoe_gated_ffn_forward", "qmoe_gated_ffn_backward")
@@ -133,6 +134,10 @@ lib.qmoe_dense_last_error.restype = ctypes.c_char_p
 lib.qmoe_dense_last_error.argtypes = []
 lib.qmoe_dense_read_device_status.restype = ctypes.c_int
 lib.qmoe_dense_read_device_status.argtypes = [_vp, _vp]
+lib.qmoe_dense_take_device_status.restype = ctypes.c_int
+lib.qmoe_dense_take_device_status.argtypes = [_vp]
+lib.qmoe_dense_set_option.restype = ctypes.c_int
+lib.qmoe_dense_set_option.argtypes = [_i32, _i64]
 lib.qmoe_mx4_quantize.restype = ctypes.c_int
 lib.qmoe_mx4_quantize.argtypes = [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _vp]
 lib.qmoe_mx4_dequantize.restype = ctypes.c_int
@@ -338,6 +343,14 @@ def _check_dense(status: int):
 
 def qmoe_dense_read_device_status(workspace, stream=None) -> int:
     return int(lib.qmoe_dense_read_device_status(_ptr(workspace), _stream(stream)))
+
+
+def qmoe_dense_take_device_status(stream=None) -> int:
+    return int(lib.qmoe_dense_take_device_status(_stream(stream)))
+
+
+def qmoe_dense_set_option(option: int, value: int):
+    _check_dense(lib.qmoe_dense_set_option(option, value))
 
 
 def qmoe_mx4_quantize(x, dtype: int, rows: int, K: int, ldx: int, codes, scales, stream=None):
