@@ -19,14 +19,15 @@ pytestmark = pytest.mark.gpu
 # roundings (of 2^-24), which its exponential turns into |z| times as much, and
 # the fast exponential is off by (2 + 1.17 |z|) 2^-23 by itself; beyond |z| = 88
 # the sigmoid has left the normal numbers. 88 (5 2^-24 + 1.17 2^-23) is below
-# 2^-14.
+# 2^-14. The normal distribution function at |g| <= 12: its
+# exponential of -g^2 / 2 >= -72 by the same count is off by less than
+# 72 (2 2^-24 + 1.17 2^-23) < 2^-15.7, and 2^-18 is left for what multiplies it.
 REL = 2.0 ** -14
 GONE = 1e-35       # what is left of a product of g beyond 88 / |z / g|
 HALF = ref.HALF[BF]
 
 RANGE = [0.0, 0.5, 1.0, 1.28, 2.0, 5.0, 20.0, 80.0, 88.0, 100.0, 1e4, 1e13, 1.8e19, 1.9e19, 1e20, 1e30, 1e38]
 EVERYWHERE = RANGE + [-v for v in RANGE[1:]]
-WHOLE = [k for k in KINDS if k != (ref.GELU, 0)]
 
 
 def _table(dense, gates, T, fusion, kind, tanh, opts):  # noqa: F811
@@ -81,7 +82,7 @@ def _check_table(dense, gates, T, fusion, kind, tanh, opts):  # noqa: F811
 
 @pytest.mark.parametrize("T", [3, 150])
 @pytest.mark.parametrize("fusion", [1, 2])
-@pytest.mark.parametrize("kind,tanh,opts", [(*k, {}) for k in WHOLE] + [
+@pytest.mark.parametrize("kind,tanh,opts", [(*k, {}) for k in KINDS] + [
     (3, 0, SWIGLU_OPTS), (3, 0, dict(activation_alpha=1.702, activation_beta=1.0, swiglu_limit=7.0)),
     (3, 0, dict(activation_alpha=1.702, activation_beta=1.0)), (3, 0, dict(activation_alpha=-0.75))],
     ids=lambda v: "-".join(f"{k.split('_')[1]}{x}" for k, x in v.items()) or "plain" if isinstance(v, dict) else str(v))
@@ -103,3 +104,11 @@ def test_gate_of_infinity(dense, kind, tanh, opts, T):  # noqa: F811
     y = dense.GatedFFN(H, I, activation_type=kind, gelu_mode=tanh, **opts)(
         x, w1, torch.ones(H, I, dtype=BF, device="cuda"), b1)
     assert (torch.isfinite(y) if opts else torch.isposinf(y)).all()
+
+
+@pytest.mark.parametrize("T", [3, 150])
+@pytest.mark.parametrize("fusion", [1, 2])
+@pytest.mark.parametrize("tanh", [0, 1], ids=["erf", "tanh"])
+def test_gelu_keeps_its_tail(dense, tanh, fusion, T):  # noqa: F811
+    """Small values of large negative gates, relative to their own size."""
+    _check_table(dense, [-0.1 * k for k in range(121)], T, fusion, ref.GELU, tanh, {})
