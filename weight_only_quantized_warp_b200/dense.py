@@ -12,6 +12,10 @@ runs in the library (``include/qmoe.h`` has the formulas) on the current
 stream of the tensors' device. Every call allocates its own workspace from
 torch's allocator, so calls on several streams and captured graphs share none.
 
+No call records an autograd graph. The block's gradients come from
+``forward_train`` and ``backward``; a call that only serves refuses tensors that
+require grad where autograd is on, instead of dropping their gradients.
+
 Device waits in the products are bounded (two seconds); results are valid when
 ``check_device_status``, called after them, returns.
 """
@@ -47,6 +51,14 @@ def _gpu(t, name) -> int:
     if index < 0:
         raise ValueError(f"{name} must be on a GPU, not on {t.device}")
     return index
+
+
+def _serves(*tensors):
+    """Refuse tensors whose gradients a call without a backward pass would drop."""
+    for t in tensors:
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
+            raise ValueError("an operand requires grad, and this call records no graph: run it under torch.no_grad() or "
+                             "on detached tensors (a GatedFFN's gradients come from forward_train and backward)")
 
 
 def _enqueue(index, call, *args):
@@ -135,6 +147,7 @@ def mx4_dequantize(codes, scales, dtype=torch.bfloat16):
 def mx4_linear(x_codes, x_scales, w_codes, w_scales, bias=None, dtype=torch.bfloat16):
     """y [..., N] = deq(x) deq(w)^T + bias for MX4 rows x [..., K] and w [N, K];
     bias and y are ``dtype``."""
+    _serves(bias)
     code = _dtype_code(dtype)
     K = _check_mx4(x_codes, x_scales, "x_")
     if _check_mx4(w_codes, w_scales, "w_") != K or w_codes.dim() != 2 or not w_codes.shape[0]:
@@ -167,6 +180,7 @@ class MX4Linear:
         self.out_features = w_codes.shape[0]
         if bias is not None:
             _tensor(bias, "bias", (self.out_features,), bias.dtype, w_codes.get_device())
+            bias = bias.detach()
         self.w_codes, self.w_scales, self.bias = w_codes, w_scales, bias
 
     @classmethod
@@ -174,6 +188,7 @@ class MX4Linear:
         return cls(*mx4_quantize(w), bias)
 
     def forward(self, x):
+        _serves(x)
         code, shape, K, N, bias = _dtype_code(x.dtype), x.shape, self.in_features, self.out_features, self.bias
         index = _gpu(x, "x")
         if not shape or shape[-1] != K or self.w_codes.get_device() != index:
@@ -250,6 +265,7 @@ class GatedFFN:
 
     def forward(self, x, w1, w2, b1=None, b2=None):
         """y, shaped like x [..., H]."""
+        _serves(x, w1, w2, b1, b2)
         return self._forward(x, w1, w2, b1, b2, False)[0]
 
     __call__ = forward
