@@ -607,7 +607,8 @@ QMOE_API qmoe_status qmoe_gated_ffn_forward(const qmoe_gated_ffn_config* cfg, in
 /*
  * qmoe_gated_ffn_backward -- from dy [T, H] and the forward's x, weights and
  * gu: dh = dy w2; dgu = the activation's derivatives times dh (at a clamp's
- * limit the slope is 1, beyond it 0; relu's slope at 0 is 0);
+ * limit the slope is 1, beyond it 0; relu's slope at 0 is 0); db1 sums the
+ * unrounded fp32 dgu;
  *   dx  [T, H]  = dgu w1        dw1 [2I, H] = dgu^T x    db1 [2I] = sum_t dgu
  *                               dw2 [H, I]  = dy^T h     db2 [H]  = sum_t dy
  * all act_dtype, written (not added to); any may be NULL to skip it. T = 0

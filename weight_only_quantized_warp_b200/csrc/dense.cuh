@@ -229,6 +229,7 @@ struct DenseArgs {
     void* out;             // kEpiStore: [M, N]; kEpiGate, kEpiGateBwd: h
     float* gu;             // kEpiGate: written when not null; kEpiGateBwd: read
     void* dgu;             // kEpiGateBwd
+    float* sums;           // kEpiGateBwd: [dense_sum_rows, 2N], sums over tokens of the unrounded dgu; nullable
     GateParams gate;
     int interleaved;       // gate and up interleaved in w1 / gu (else concatenated)
     int32_t* status;       // workspace status word; reset by the call's first product
@@ -261,14 +262,26 @@ inline bool dense_streams(int64_t M, int64_t b_bytes) {
 }
 cudaError_t launch_dense_stream(const DenseArgs& a, bool early, cudaStream_t st);
 
-// out[n] = sum_m x[m, n] (x [M, N] bf16, out bf16; skipped when out is null) in a
-// fixed order, for up to two matrices; part: workspace of colsum_bytes.
+// Rows of DenseArgs::sums that a product of few rows or of many writes (one for
+// each split of K, which finishes some of the tokens, or for 32 tokens), and the
+// most that it may be.
+int64_t dense_stream_splits(const DenseArgs& a);
+inline int64_t dense_sum_rows(const DenseArgs& a) {
+    return dense_streams(a.M, a.N * a.K * 2) ? dense_stream_splits(a) : (a.M + 31) / 32;
+}
+inline int64_t dense_sum_rows_most(int64_t M, int64_t N, int64_t K) {
+    return dense_streams(M, N * K * 2) ? 8 : (M + 31) / 32;
+}
+
+// out[n] = sum_m x[m, n] (x [M, N] fp32 or bf16, out bf16; skipped when out is
+// null) in a fixed order, for up to two matrices: an fp32 and a bf16 one; part:
+// workspace of colsum_bytes.
 struct ColSum {
     const void* x;
-    int64_t N;
+    int64_t M, N;
     void* out;
 };
-size_t colsum_bytes(int64_t M, int64_t Na, int64_t Nb);
-cudaError_t launch_colsum(const ColSum& a, const ColSum& b, int64_t M, float* part, cudaStream_t st);
+size_t colsum_bytes(int64_t Ma, int64_t Na, int64_t Mb, int64_t Nb);
+cudaError_t launch_colsum(const ColSum& f32, const ColSum& bf16, float* part, cudaStream_t st);
 
 }  // namespace qmoe

@@ -115,12 +115,14 @@ qmoe_status check_ffn(const qmoe_gated_ffn_config* c, int64_t T, GateParams* g) 
 }
 
 struct FfnLayout : Layout {
-    size_t h = 0, dgu = 0, part = 0;
+    size_t h = 0, dgu = 0, sums = 0, part = 0;
     FfnLayout(const qmoe_gated_ffn_config& c, int64_t T, bool backward) {
         h = take(size_t(T) * c.inter_size * 2);
         if (backward) {
             dgu = take(size_t(T) * c.inter_size * 4);
-            part = take(colsum_bytes(T, 2 * c.inter_size, c.hidden_size));
+            const int64_t rows = dense_sum_rows_most(T, c.inter_size, c.hidden_size);
+            sums = take(size_t(rows) * c.inter_size * 8);
+            part = take(colsum_bytes(rows, 2 * c.inter_size, T, c.hidden_size));
         }
     }
 };
@@ -418,7 +420,8 @@ qmoe_status qmoe_gated_ffn_backward(const qmoe_gated_ffn_config* cfg, int64_t T,
     if (qmoe_status s = on_current_device(first)) return s;
     char* ws = (char*)workspace;
     void *h = ws + l.h, *dgu = ws + l.dgu;
-    float* part = (float*)(ws + l.part);
+    float *sums = (float*)(ws + l.sums), *part = (float*)(ws + l.part);
+    int64_t sum_rows = 0;
     cudaError_t e = cudaSuccess;
     auto product = [&](DenseOperand oa, DenseOperand ob, int64_t M, int64_t N, int64_t K, void* out) {
         DenseArgs a{};
@@ -443,10 +446,12 @@ qmoe_status qmoe_gated_ffn_backward(const qmoe_gated_ffn_config* cfg, int64_t T,
         a.out = h;
         a.gu = const_cast<float*>(gu);
         a.dgu = dgu;
+        a.sums = db1 ? sums : nullptr;
         a.gate = gate;
         a.interleaved = cfg->swiglu_fusion == 1;
         a.status = (int32_t*)workspace;
         a.reset_status = 1;
+        sum_rows = dense_sum_rows(a);
         e = launch_rows(a, false, st);
     } else if (e == cudaSuccess) {
         e = cudaMemsetAsync(workspace, 0, 4, st);
@@ -459,7 +464,7 @@ qmoe_status qmoe_gated_ffn_backward(const qmoe_gated_ffn_config* cfg, int64_t T,
     // h comes from the kernel before dx: known to be complete after dx's launch only
     if (e == cudaSuccess && ((dx && !stream_dx) || dw1 || dw2))
         e = launch_dense_pairs(dx && !stream_dx ? &pdx : nullptr, dw1 ? &pw1 : nullptr, dw2 ? &pw2 : nullptr, stream_dx, st);
-    if (e == cudaSuccess) e = launch_colsum({dgu, 2 * I, db1}, {dy, H, db2}, T, part, st);
+    if (e == cudaSuccess) e = launch_colsum({sums, sum_rows, 2 * I, db1}, {dy, T, H, db2}, part, st);
     return e == cudaSuccess ? QMOE_OK : cuda_bad(e, "gated_ffn_backward");
 }
 

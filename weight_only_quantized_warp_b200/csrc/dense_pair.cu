@@ -59,6 +59,7 @@ struct PairArgs {
     const void* bias;
     float* gu;
     void* dgu;
+    float* sums;
     GateParams gate;
     int32_t* status;
     int reset_status;
@@ -502,6 +503,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
                 };
                 with_gate_mode(a.gate, [&](auto mode) {
                     float4 xs[4], ys[4];
+                    float ag[4], au[4];  // the lane's columns over the block's rows
 #pragma unroll
                     for (int k = 0; k < 4; ++k) load_gu(k, xs[k], ys[k]);
 #pragma unroll 1
@@ -510,6 +512,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
                             float v[32];
                             tmem_f32(tb + uint32_t(half * 32 + 8 * s0), v);
                             put_f32(turn, lane, v);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) ag[k] = au[k] = 0.0f;
                         }
 #pragma unroll
                         for (int k4 = 0; k4 < 4; ++k4) {
@@ -533,6 +537,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
                             const int64_t col = c0 + 64 * (s >> 3);
                             if (4 * (s & 7) + r0 < rows && col < end) {  // N is a multiple of 8: whole fours
                                 const int64_t row = m0 + r0 + 4 * (s & 7);
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    ag[k] += dg[k];
+                                    au[k] += du[k];
+                                }
                                 *reinterpret_cast<uint2*>((__nv_bfloat16*)p.out + row * N + col) =
                                     make_uint2(pack_bf16(h[0], h[1]), pack_bf16(h[2], h[3]));
                                 __nv_bfloat16* d = (__nv_bfloat16*)a.dgu + row * 2 * N + (a.interleaved ? 2 * col : col);
@@ -546,6 +555,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
                                 }
                             }
                             load_gu(min(s + 4, steps - 1), xs[k4], ys[k4]);
+                        }
+                        if ((s0 & 4) && a.sums) {
+                            // each of the four lanes of the same columns ends with one column's g and u
+                            const bool hi = lane & 16, odd = lane & 8;
+                            float p[2], q[2];
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                p[k] = (hi ? ag[2 + k] : ag[k]) + __shfl_xor_sync(0xffffffffu, hi ? ag[k] : ag[2 + k], 16);
+                                q[k] = (hi ? au[2 + k] : au[k]) + __shfl_xor_sync(0xffffffffu, hi ? au[k] : au[2 + k], 16);
+                            }
+                            const float sg = (odd ? p[1] : p[0]) + __shfl_xor_sync(0xffffffffu, odd ? p[0] : p[1], 8);
+                            const float su = (odd ? q[1] : q[0]) + __shfl_xor_sync(0xffffffffu, odd ? q[0] : q[1], 8);
+                            const int64_t col = c0 + 64 * (s0 >> 3) + (hi ? 2 : 0) + (odd ? 1 : 0);
+                            if (rows > 0 && col < end) {
+                                float* o = a.sums + (m0 >> 5) * 2 * N;
+                                o[a.interleaved ? 2 * col : col] = sg;
+                                o[a.interleaved ? 2 * col + 1 : N + col] = su;
+                            }
                         }
                         __syncwarp();
                     }
@@ -669,6 +696,7 @@ cudaError_t launch_dense_pair(const DenseArgs& d, bool early, cudaStream_t st) {
     a.bias = d.bias;
     a.gu = d.gu;
     a.dgu = d.dgu;
+    a.sums = d.sums;
     a.gate = d.gate;
     a.status = d.status;
     a.reset_status = d.reset_status;

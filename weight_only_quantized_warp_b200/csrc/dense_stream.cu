@@ -40,6 +40,7 @@ struct StreamArgs {
     void* out;
     float* gu;             // kEpiGate: written when not null; kEpiGateBwd: read
     __nv_bfloat16* dgu;    // kEpiGateBwd
+    float* sums;           // kEpiGateBwd: [splits, 2N] when not null
     GateParams gate;
     int32_t* status;
     int reset_status;
@@ -68,10 +69,11 @@ struct StreamCfg {
 };
 
 // The results of W row n for up to NB tokens from t on, of which `left` exist:
-// g (and u, for the gate) are their sums.
+// g (and u, for the gate) are their sums. kEpiGateBwd adds dgu to ag and au.
 template <int EPI, int NB>
 __device__ __forceinline__ void stream_emit(const StreamArgs& a, int t, int left, int64_t n,
-                                            const float (&g)[NB], const float (&u)[NB], float bg, float bu) {
+                                            const float (&g)[NB], const float (&u)[NB], float bg, float bu, float& ag,
+                                            float& au) {
     float sg[NB], su[NB];
     if (EPI == kEpiGateBwd) {  // all loads before any use
 #pragma unroll
@@ -97,8 +99,11 @@ __device__ __forceinline__ void stream_emit(const StreamArgs& a, int t, int left
         } else if (EPI == kEpiGateBwd) {
             float hg, hu;
             *ob = __float2bfloat16_rn(gate_slopes<-1, true>(a.gate, sg[j], su[j], hg, hu));
-            a.dgu[gi] = __float2bfloat16_rn(g[j] * hg);
-            a.dgu[ui] = __float2bfloat16_rn(g[j] * hu);
+            const float dg = g[j] * hg, du = g[j] * hu;
+            ag += dg;
+            au += du;
+            a.dgu[gi] = __float2bfloat16_rn(dg);
+            a.dgu[ui] = __float2bfloat16_rn(du);
         } else if (a.out_f32) {
             reinterpret_cast<float*>(a.out)[tt * a.N + n] = g[j] + bg;
         } else {
@@ -287,6 +292,7 @@ __global__ void __launch_bounds__(kSThreads, StreamCfg<MX4, EPI == kEpiGate, NT>
             __syncwarp();
             cluster_sync_all();  // every ring has drained
         }
+        float ag = 0.0f, au = 0.0f;  // kEpiGateBwd: over this rank's tokens
         if (ok) {
             const uint32_t mine = smem_u32(part + rank * per * NACC * 128 + row);
             int owner = 0, slot = 0;
@@ -305,7 +311,7 @@ __global__ void __launch_bounds__(kSThreads, StreamCfg<MX4, EPI == kEpiGate, NT>
                         if (++slot == per) { slot = 0; ++owner; }
                     }
                 } else if (valid) {
-                    stream_emit<EPI, 16>(a, t0, a.T - t0, n, v, u, bg, bu);
+                    stream_emit<EPI, 16>(a, t0, a.T - t0, n, v, u, bg, bu, ag, au);
                 }
                 __syncwarp();
             }
@@ -325,9 +331,14 @@ __global__ void __launch_bounds__(kSThreads, StreamCfg<MX4, EPI == kEpiGate, NT>
                             u[0] += y.x; u[1] += y.y; u[2] += y.z; u[3] += y.w;
                         }
                     }
-                    stream_emit<EPI, 4>(a, t, a.T - t, n, g, u, bg, bu);
+                    stream_emit<EPI, 4>(a, t, a.T - t, n, g, u, bg, bu, ag, au);
                 }
             }
+        }
+        if (EPI == kEpiGateBwd && a.sums && valid) {
+            float* o = a.sums + int64_t(rank) * 2 * a.N;
+            o[a.interleaved ? 2 * n : n] = ag;
+            o[a.interleaved ? 2 * n + 1 : a.N + n] = au;
         }
     }
     if (a.splits > 1 && warp < 2) {
@@ -384,6 +395,17 @@ cudaError_t dense_stream_gave_up(uint32_t* count, cudaStream_t st) {
     return cudaMemcpyFromSymbolAsync(count, g_stream_gave_up, sizeof *count, 0, cudaMemcpyDeviceToHost, st);
 }
 
+// Splits of K: as many (a cluster holds 8) as keep all CTAs resident and every
+// split at least two stages long.
+int64_t dense_stream_splits(const DenseArgs& d) {
+    const bool gate = d.epi == kEpiGate;
+    const int64_t tiles = ((gate ? d.N / 2 : d.N) + 127) / 128, nks = (d.K + (d.mx4 ? 255 : 63)) / (d.mx4 ? 256 : 64);
+    const int64_t slots = (gate && d.M > 64 ? 1 : 2) * sm_count();
+    int64_t splits = 1;
+    while (splits < 8 && tiles * (splits + 1) <= slots && nks >= 2 * (splits + 1)) ++splits;
+    return splits;
+}
+
 cudaError_t launch_dense_stream(const DenseArgs& d, bool early_w, cudaStream_t st) {
     const bool gate = d.epi == kEpiGate;
     StreamArgs a{};
@@ -400,16 +422,13 @@ cudaError_t launch_dense_stream(const DenseArgs& d, bool early_w, cudaStream_t s
     a.out = d.out;
     a.gu = d.gu;
     a.dgu = (__nv_bfloat16*)d.dgu;
+    a.sums = d.sums;
     a.gate = d.gate;
     a.status = d.status;
     a.reset_status = d.reset_status;
     a.waits = dense_waits();
     const int64_t tiles = (a.N + 127) / 128;
-    // Splits of K: as many (a cluster holds 8) as keep all CTAs resident and
-    // every split at least two stages long.
-    const int64_t slots = (gate && d.M > 64 ? 1 : 2) * sm_count();
-    a.splits = 1;
-    while (a.splits < 8 && tiles * (a.splits + 1) <= slots && a.nks >= 2 * (a.splits + 1)) ++a.splits;
+    a.splits = int(dense_stream_splits(d));
     if (tiles * a.splits > (int64_t(1) << 30)) return cudaErrorInvalidValue;
     const uint32_t nt = d.M <= 16 ? 16 : d.M <= 32 ? 32 : d.M <= 64 ? 64 : 128;
     CUtensorMap wmap, xmap;
