@@ -208,13 +208,14 @@ __device__ __forceinline__ float4 ld_early(const float* p) {
     asm volatile("ld.global.cs.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
     return v;
 }
-// AMN: A MN-major (0, 1, or 2: as each product says).
-template <bool MX4, int AMN, bool BMN, int EPI>
+
+// MULTI: several products, whose A lies as each says; else A lies along k. BMN: B
+// lies across its rows.
+template <bool MX4, bool MULTI, bool BMN, int EPI>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
     dense_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ PairArgs a) {
     using C = PairCfg<MX4>;
     constexpr int ST = C::kStages;
-    constexpr bool MULTI = AMN == 2;
     extern __shared__ uint8_t smem_raw[];
     // the dynamic segment starts at the same address in both CTAs, so the
     // aligned offsets agree
@@ -292,7 +293,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
                 const uint32_t sa = stage0 + s * C::kStage, fb = full0 + 8 * s;
                 const int m0 = tm * 256 + int(rank) * 128;
                 const CUtensorMap* m = &maps.a[MULTI ? q : 0];
-                if (AMN == 1 || (MULTI && a.p[MULTI ? q : 0].amn)) {
+                if (MULTI && a.p[MULTI ? q : 0].amn) {
                     tma_3d_pair(sa, m, m0, ks * 64, 0, fb);
                     tma_3d_pair(sa + 8192, m, m0 + 64, ks * 64, 0, fb);
                 } else {
@@ -340,7 +341,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
                 if (!mbar_wait_cluster(smem_u32(&acce[acc]), cph ^ 1u, abort_flag, a.status, a.waits.limit_ns)) break;
                 tc_fence_after();
                 const int BN = a.p[MULTI ? q : 0].bn, nks = a.p[MULTI ? q : 0].nks;
-                const bool amn = AMN == 1 || (MULTI && a.p[MULTI ? q : 0].amn);
+                const bool amn = MULTI && a.p[MULTI ? q : 0].amn;
                 const uint32_t idesc = idesc_f16(256, BN, amn, BMN);
                 const uint32_t d = tmem + uint32_t(acc * C::BN);
                 for (int ks = 0; ks < nks; ++ks) {
@@ -598,10 +599,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
     }
 }
 
-template <bool MX4, int AMN, bool BMN, int EPI>
+template <bool MX4, bool MULTI, bool BMN, int EPI>
 cudaError_t launch_one(const PairMaps& maps, PairArgs& a, cudaStream_t st) {
     a.waits = dense_waits();
-    constexpr auto kern = dense_pair_kernel<MX4, AMN, BMN, EPI>;
+    constexpr auto kern = dense_pair_kernel<MX4, MULTI, BMN, EPI>;
     cudaError_t e = raise_smem<kern>(PairCfg<MX4>::kSmem);
     if (e != cudaSuccess) return e;
     const int64_t tiles = int64_t(a.tiles[0]) + a.tiles[1] + a.tiles[2], pairs = sm_count() / 2;
@@ -722,12 +723,12 @@ cudaError_t launch_dense_pair(const DenseArgs& d, bool early, cudaStream_t st) {
             sc.box[2] = 1;
             if ((e = encode_map(i ? &maps.b[1] : &maps.a[1], sc)) != cudaSuccess) return e;
         }
-        return launch_one<true, 0, false, kEpiStore>(maps, a, st);
+        return launch_one<true, false, false, kEpiStore>(maps, a, st);
     }
     if ((e = bf16_maps(maps, 0, d, a.p[0])) != cudaSuccess) return e;
-    if (d.epi == kEpiGate) return launch_one<false, 0, false, kEpiGate>(maps, a, st);
-    if (d.epi == kEpiGateBwd) return launch_one<false, 0, true, kEpiGateBwd>(maps, a, st);
-    return launch_one<false, 0, false, kEpiStore>(maps, a, st);
+    if (d.epi == kEpiGate) return launch_one<false, false, false, kEpiGate>(maps, a, st);
+    if (d.epi == kEpiGateBwd) return launch_one<false, false, true, kEpiGateBwd>(maps, a, st);
+    return launch_one<false, false, false, kEpiStore>(maps, a, st);
 }
 
 cudaError_t launch_dense_pairs(const DenseArgs* first, const DenseArgs* second, const DenseArgs* third, bool early3,
@@ -753,7 +754,7 @@ cudaError_t launch_dense_pairs(const DenseArgs* first, const DenseArgs* second, 
         const int64_t most = (W + short_of - 1) / short_of;
         a.head = int(head < most ? head : most);
     }
-    return launch_one<false, 2, true, kEpiStore>(maps, a, st);
+    return launch_one<false, true, true, kEpiStore>(maps, a, st);
 }
 
 }  // namespace qmoe
