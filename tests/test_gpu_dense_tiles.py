@@ -45,3 +45,21 @@ def test_mx4_rounding_by_the_c_call(dense, bf16):  # noqa: F811
     assert torch.equal(codes[16:16 + 7 * 48].view(7, 48), rc) and torch.equal(scales[5:26].view(7, 3), rs)
     assert (codes[:16] == 9).all() and (codes[16 + 7 * 48:] == 9).all()
     assert (scales[:5] == 9).all() and (scales[26:] == 9).all()
+
+
+@pytest.mark.parametrize("T", [1, 40, 200])
+def test_mx4_slices_at_any_address(dense, T):  # noqa: F811
+    """Rows of stacked codes and scales whose addresses the products do not take
+    as they are: 3 scales a row, and views off the 16 bytes."""
+    n = _gen(T)
+    xc, xs = dense.mx4_quantize(n(T + 1, 96))
+    wc, ws = dense.mx4_quantize(n(2, 51, 96))
+    bias = n(51).to(torch.bfloat16)
+    copies = [t.clone() for t in (xc[1:], xs[1:], wc[1], ws[1])]
+    want = dense.mx4_linear(*copies, bias)
+    assert ws[1].data_ptr() % 4 and torch.equal(dense.mx4_linear(xc[1:], xs[1:], wc[1], ws[1], bias), want)
+    assert torch.equal(dense.MX4Linear(wc[1], ws[1], bias)(dense.mx4_dequantize(xc[1:], xs[1:])),
+                       dense.MX4Linear(*copies[2:], bias)(dense.mx4_dequantize(*copies[:2])))
+    odd = torch.empty(xc[1:].numel() + 1, dtype=torch.uint8, device="cuda")[1:].view(T, 48).copy_(xc[1:])
+    assert torch.equal(dense.mx4_linear(odd, xs[1:], *copies[2:], bias), want)
+    assert torch.equal(dense.mx4_dequantize(odd, xs[1:]), dense.mx4_dequantize(*copies[:2]))

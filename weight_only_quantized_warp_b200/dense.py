@@ -100,6 +100,12 @@ def _rows(x):
     return x, ldx
 
 
+def _aligned(codes, scales):
+    """MX4 rows at the addresses the products take (a slice's need not be):
+    copies of what is off them."""
+    return (codes.clone() if codes.data_ptr() % 16 else codes), (scales.clone() if scales.data_ptr() % 4 else scales)
+
+
 def mx4_quantize(x):
     """x [..., K] (float32 or bfloat16, K a multiple of 32) to ``(codes, scales)``:
     uint8 [..., K/2] and [..., K/32]. A 2-D x with unit stride along K and
@@ -137,6 +143,7 @@ def mx4_dequantize(codes, scales, dtype=torch.bfloat16):
     code = _dtype_code(dtype)
     K = _check_mx4(codes, scales, "")
     index = _gpu(codes, "codes")
+    codes, scales = _aligned(codes, scales)
     x = codes.new_empty((*codes.shape[:-1], K), dtype=dtype)
     rows = x.numel() // K
     if rows:
@@ -158,6 +165,7 @@ def mx4_linear(x_codes, x_scales, w_codes, w_scales, bias=None, dtype=torch.bflo
     if bias is not None:
         _tensor(bias, "bias", (N,), dtype, index)
     _gpu(x_codes, "x_codes")
+    (x_codes, x_scales), (w_codes, w_scales) = _aligned(x_codes, x_scales), _aligned(w_codes, w_scales)
     y = x_codes.new_empty((*x_codes.shape[:-1], N), dtype=dtype)
     T = y.numel() // N
     if T:
@@ -181,7 +189,8 @@ class MX4Linear:
         if bias is not None:
             _tensor(bias, "bias", (self.out_features,), bias.dtype, w_codes.get_device())
             bias = bias.detach()
-        self.w_codes, self.w_scales, self.bias = w_codes, w_scales, bias
+        self.w_codes, self.w_scales = _aligned(w_codes, w_scales)
+        self.bias = bias
 
     @classmethod
     def from_weights(cls, w, bias=None):
