@@ -15,3 +15,10 @@ def test_dense_options(option, value, status):
     if status:
         with pytest.raises(qmoe.QMoEError):
             qmoe.qmoe_dense_set_option(option, value)
+
+
+def test_device_status_is_a_gpus():
+    libbuild.build()
+    from weight_only_quantized_warp_b200 import dense
+    with pytest.raises(ValueError):
+        dense.check_device_status("cpu")

@@ -78,8 +78,10 @@ def check_device_status(device=None):
     replay on that GPU gave up since the last check: results since then are
     undefined. Work on other streams counts once it has finished. Synchronises,
     so it belongs after a step, not after every call, and not into a capture."""
-    index = torch.cuda.current_device() if device is None else torch.device(device).index
-    _enqueue(torch.cuda.current_device() if index is None else index, qmoe.lib.qmoe_dense_take_device_status)
+    device = torch.device("cuda" if device is None else device)
+    if device.type != "cuda":
+        raise ValueError(f"the status is a GPU's, not {device}'s")
+    _enqueue(torch.cuda.current_device() if device.index is None else device.index, qmoe.lib.qmoe_dense_take_device_status)
 
 
 def _address(t):
