@@ -463,7 +463,8 @@ qmoe_status qmoe_gated_ffn_backward(const qmoe_gated_ffn_config* cfg, int64_t T,
     if (e == cudaSuccess && stream_dx) e = launch_dense_stream(pdx, true, st);
     // h comes from the kernel before dx: known to be complete after dx's launch only
     if (e == cudaSuccess && ((dx && !stream_dx) || dw1 || dw2))
-        e = launch_dense_pairs(dx && !stream_dx ? &pdx : nullptr, dw1 ? &pw1 : nullptr, dw2 ? &pw2 : nullptr, stream_dx, st);
+        e = launch_dense_pairs(dx && !stream_dx ? &pdx : nullptr, dw1 ? &pw1 : nullptr, dw2 ? &pw2 : nullptr, stream_dx,
+                               st);
     if (e == cudaSuccess) e = launch_colsum({sums, sum_rows, 2 * I, db1}, {dy, T, H, db2}, part, st);
     return e == cudaSuccess ? QMOE_OK : cuda_bad(e, "gated_ffn_backward");
 }

@@ -88,9 +88,10 @@ __global__ void __launch_bounds__(256) colsum_join_kernel(const ColPair p, const
 
 int64_t col_blocks(int64_t N) { return (N + 255) / 256; }
 
-// Row ranges of a matrix: about four CTAs per SM, at least 32 rows each. They are
-// those of both sums whichever is asked for, so that either comes out the same
-// alone.
+// Row ranges of a matrix: about four CTAs for each SM of a B200 (the size of a
+// workspace follows from them and is asked for without a device), at least 32
+// rows each. They are those of both sums whichever is asked for, so that either
+// comes out the same alone.
 int col_ranges(int64_t M, int64_t Na, int64_t Nb) {
     const int64_t blocks = col_blocks(Na) + col_blocks(Nb);
     const int64_t want = (4 * 148 + blocks - 1) / blocks, most = (M + 31) / 32;

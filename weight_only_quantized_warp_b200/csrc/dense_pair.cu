@@ -25,8 +25,8 @@
 // up rows (one per CTA), so a thread holds gate and up of the same column.
 //
 // Warps (384 threads): 0 TMA, 1 MMA issue (leader CTA) and tensor memory, one
-// thread of each issuing; 4-11 epilogue. Every wait is bounded (then QMOE_TIMEOUT in the status word,
-// every role leaves its loop).
+// thread of each issuing; 4-11 epilogue. Every wait is bounded (then
+// QMOE_TIMEOUT in the status word, every role leaves its loop).
 #include "dense_tc.cuh"
 
 namespace qmoe {
@@ -59,7 +59,7 @@ struct PairArgs {
     const void* bias;
     float* gu;
     void* dgu;
-    float* sums;
+    float* sums;           // see DenseArgs
     GateParams gate;
     int32_t* status;
     int reset_status;
@@ -321,7 +321,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
             }
             for (int i = 0; ok && tile_at<MULTI>(a, i, q, tm, tn); ++i) {
                 for (; ks < a.p[MULTI ? q : 0].nks; ++ks) {
-                    if (!mbar_wait(smem_u32(&empty[st]), ph ^ 1u, abort_flag, a.status, a.waits.limit_ns)) { ok = false; break; }
+                    ok = mbar_wait(smem_u32(&empty[st]), ph ^ 1u, abort_flag, a.status, a.waits.limit_ns);
+                    if (!ok) break;
                     load_b(q, tn, ks, st);
                     load_a(q, tm, tn, ks, st);
                     if (++st == ST) { st = 0; ph ^= 1u; }
@@ -345,7 +346,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
                 const uint32_t idesc = idesc_f16(256, BN, amn, BMN);
                 const uint32_t d = tmem + uint32_t(acc * C::BN);
                 for (int ks = 0; ks < nks; ++ks) {
-                    if (!mbar_wait_cluster(smem_u32(&full[st]), ph, abort_flag, a.status, a.waits.limit_ns)) { ok = false; break; }
+                    ok = mbar_wait_cluster(smem_u32(&full[st]), ph, abort_flag, a.status, a.waits.limit_ns);
+                    if (!ok) break;
                     tc_fence_after();
                     const uint32_t sa = smem_u32(smem + st * C::kStage), sb = sa + kABytes;
                     const uint32_t acc0 = ks > 0 ? 1u : 0u;
@@ -478,7 +480,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
                     }
                     with_gate_mode(a.gate, [&](auto mode) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) g[i] = gate_value<decltype(mode)::value, decltype(mode)::clamp>(a.gate, g[i], u[i]);
+                        for (int i = 0; i < 32; ++i)
+                            g[i] = gate_value<decltype(mode)::value, decltype(mode)::clamp>(a.gate, g[i], u[i]);
                     });
                     uint4 w[4];
                     pack32(g, w);
@@ -531,7 +534,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
                                 float hg, hu;
-                                h[k] = gate_slopes<decltype(mode)::value, decltype(mode)::clamp>(a.gate, g[k], u[k], hg, hu);
+                                h[k] = gate_slopes<decltype(mode)::value, decltype(mode)::clamp>(a.gate, g[k], u[k],
+                                                                                                 hg, hu);
                                 dg[k] = dh[k] * hg;
                                 du[k] = dh[k] * hu;
                             }
@@ -545,12 +549,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
                                 }
                                 *reinterpret_cast<uint2*>((__nv_bfloat16*)p.out + row * N + col) =
                                     make_uint2(pack_bf16(h[0], h[1]), pack_bf16(h[2], h[3]));
-                                __nv_bfloat16* d = (__nv_bfloat16*)a.dgu + row * 2 * N + (a.interleaved ? 2 * col : col);
+                                const int64_t at = row * 2 * N + (a.interleaved ? 2 * col : col);
+                                __nv_bfloat16* d = (__nv_bfloat16*)a.dgu + at;
                                 if (a.interleaved) {
-                                    *reinterpret_cast<uint4*>(d) = make_uint4(pack_bf16(dg[0], du[0]), pack_bf16(dg[1], du[1]),
-                                                                              pack_bf16(dg[2], du[2]), pack_bf16(dg[3], du[3]));
+                                    *reinterpret_cast<uint4*>(d) =
+                                        make_uint4(pack_bf16(dg[0], du[0]), pack_bf16(dg[1], du[1]),
+                                                   pack_bf16(dg[2], du[2]), pack_bf16(dg[3], du[3]));
                                 } else {
-                                    *reinterpret_cast<uint2*>(d) = make_uint2(pack_bf16(dg[0], dg[1]), pack_bf16(dg[2], dg[3]));
+                                    *reinterpret_cast<uint2*>(d) =
+                                        make_uint2(pack_bf16(dg[0], dg[1]), pack_bf16(dg[2], dg[3]));
                                     *reinterpret_cast<uint2*>(d + N) =
                                         make_uint2(pack_bf16(du[0], du[1]), pack_bf16(du[2], du[3]));
                                 }
@@ -558,16 +565,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
                             load_gu(min(s + 4, steps - 1), xs[k4], ys[k4]);
                         }
                         if ((s0 & 4) && a.sums) {
-                            // each of the four lanes of the same columns ends with one column's g and u
+                            // Each of the four lanes of the same columns ends with one column's g
+                            // and u (all four sums in each lane, and whole vectors to store, took
+                            // registers that spilled: a training step 149.8 against 149.1 us).
                             const bool hi = lane & 16, odd = lane & 8;
-                            float p[2], q[2];
-#pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                p[k] = (hi ? ag[2 + k] : ag[k]) + __shfl_xor_sync(0xffffffffu, hi ? ag[k] : ag[2 + k], 16);
-                                q[k] = (hi ? au[2 + k] : au[k]) + __shfl_xor_sync(0xffffffffu, hi ? au[k] : au[2 + k], 16);
-                            }
-                            const float sg = (odd ? p[1] : p[0]) + __shfl_xor_sync(0xffffffffu, odd ? p[0] : p[1], 8);
-                            const float su = (odd ? q[1] : q[0]) + __shfl_xor_sync(0xffffffffu, odd ? q[0] : q[1], 8);
+                            auto join = [&](const float (&v)[4]) {
+                                const float x = (hi ? v[2] : v[0]) + __shfl_xor_sync(~0u, hi ? v[0] : v[2], 16);
+                                const float y = (hi ? v[3] : v[1]) + __shfl_xor_sync(~0u, hi ? v[1] : v[3], 16);
+                                return (odd ? y : x) + __shfl_xor_sync(~0u, odd ? x : y, 8);
+                            };
+                            const float sg = join(ag), su = join(au);
                             const int64_t col = c0 + 64 * (s0 >> 3) + (hi ? 2 : 0) + (odd ? 1 : 0);
                             if (rows > 0 && col < end) {
                                 float* o = a.sums + (m0 >> 5) * 2 * N;
@@ -615,10 +622,13 @@ cudaError_t launch_one(const PairMaps& maps, PairArgs& a, cudaStream_t st) {
 // last, half-empty one: the width (a multiple of 32, at least 128) with the
 // smallest rounds x (BN + 256), a stage's operand bytes per CTA, which is what a
 // stage takes below 256 columns. Measured at T = 1024, H = I = 2880 (160
-// columns) against 256 throughout: forward 56.7 against 67.6 us, training step
-// 194 against 217 us; 160 columns at T = 4096, H = 4096, I = 14336 (where the
-// rule keeps 256) take 3792 us against 3120.
-// A second product of the same launch counts its tiles too.
+// columns) against 256 throughout: forward 46 against 56 us, training step 148
+// against 158; 160 columns at T = 4096, H = 4096, I = 14336 (where the rule
+// keeps 256) take 4080 us against 3390. MX4 at T = 1001, N = 2817 (160 columns)
+// against 240: 13.3 against 15.0 us.
+// A second product of the same launch counts its tiles too. The 74 pairs of a
+// B200 are planned for whatever the device has, because the size of a workspace
+// follows from the width and is asked for without a device.
 int pair_width(int64_t tiles_m, int64_t n, bool mx4, int64_t tiles_m2 = 0, int64_t n2 = 0) {
     constexpr int64_t kPairs = 74;
     int best = 0;

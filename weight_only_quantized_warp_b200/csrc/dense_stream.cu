@@ -251,8 +251,10 @@ __global__ void __launch_bounds__(kSThreads, StreamCfg<MX4, EPI == kEpiGate, NT>
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     if (ks + i >= ks1) break;
-                    if (!warp_wait(smem_u32(&empty[st]), ph ^ 1u, abort_flag, a.status, a.waits.limit_ns)) { ok = false; break; }
-                    uint32_t* sc = reinterpret_cast<uint32_t*>(smem + st * C::kStage + kSW + C::kX) + (et & 31) * 4 + (et >> 5);
+                    ok = warp_wait(smem_u32(&empty[st]), ph ^ 1u, abort_flag, a.status, a.waits.limit_ns);
+                    if (!ok) break;
+                    uint32_t* sc = reinterpret_cast<uint32_t*>(smem + st * C::kStage + kSW + C::kX) +
+                                   (et & 31) * 4 + (et >> 5);
                     sc[0] = cw[2 * i];
                     sc[128] = cw[2 * i + 1];
                     if (et < NT) {
